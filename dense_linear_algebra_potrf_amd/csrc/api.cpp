@@ -11,27 +11,24 @@
 
 #include <hip/hip_runtime.h>
 
-#include <atomic>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
-#include <exception>
 #include <mutex>
 #include <string>
 
 #include "families.hpp"
+#include "status.hpp"
 
 namespace {
 
 using bl::DT;
 using bl::Geometry;
-
-thread_local std::string g_last_error;
-
-batchlas_status fail(batchlas_status s, const std::string& msg) {
-    g_last_error = msg;
-    return s;
-}
+using bl::check_device;
+using bl::fail;
+using bl::guarded;
+using bl::hip_status;
+using bl::mul_ok;
 
 // ---------------------------------------------------------------- environment snapshot
 struct EnvSnapshot {
@@ -132,8 +129,6 @@ int auto_tiny_cut(DT dt) {
 }
 
 // ---------------------------------------------------------------- validation
-bool mul_ok(int64_t a, int64_t b, int64_t& out) { return !__builtin_mul_overflow(a, b, &out); }
-
 batchlas_status check_common(int dt, int uplo, int64_t n, int64_t nrhs, bool is_posv,
                              int64_t lda, int64_t strideA, int64_t ldb, int64_t strideB,
                              int64_t batch, const void* A, const void* B, bool check_ptrs) {
@@ -280,31 +275,7 @@ void trace(const char* op, DT dt, int uplo, int64_t n, int64_t nrhs, int64_t bat
                  g.threads, g.panel, (long long)g.grid, (long long)g.lds);
 }
 
-// ---------------------------------------------------------------- device check
-// The library carries gfx950 code only; refuse other devices up front.
-batchlas_status check_device() {
-    static std::atomic<int> state[64];
-    int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess)
-        return fail(BATCHLAS_HIP_ERROR, "hipGetDevice failed");
-    if (dev < 0 || dev >= 64) return fail(BATCHLAS_NOT_SUPPORTED, "device index out of range");
-    int s = state[dev].load(std::memory_order_acquire);
-    if (s == 0) {
-        hipDeviceProp_t prop;
-        if (hipGetDeviceProperties(&prop, dev) != hipSuccess)
-            return fail(BATCHLAS_HIP_ERROR, "hipGetDeviceProperties failed");
-        s = std::strncmp(prop.gcnArchName, "gfx950", 6) == 0 ? 1 : 2;
-        state[dev].store(s, std::memory_order_release);
-    }
-    if (s != 1) return fail(BATCHLAS_NOT_SUPPORTED, "this library is built for gfx950 only");
-    return BATCHLAS_OK;
-}
-
-batchlas_status hip_status(hipError_t e, const char* what) {
-    if (e == hipSuccess) return BATCHLAS_OK;
-    return fail(BATCHLAS_HIP_ERROR, std::string(what) + ": " + hipGetErrorString(e));
-}
-
+// ---------------------------------------------------------------- the operations
 batchlas_status do_potrf(int family, int dt_, int uplo, int64_t n, void* A, int64_t lda,
                          int64_t strideA, int64_t batch, int32_t* info, batchlas_stream_t stream) {
     batchlas_status st = check_common(dt_, uplo, n, 0, false, lda, strideA, 0, 0, batch, A,
@@ -357,17 +328,6 @@ batchlas_status do_posv(int family, int dt_, int uplo, int64_t n, int64_t nrhs, 
     return hip_status(bl::potrs(dt, upper, int(n), int(nrhs), A, lda, strideA, B, ldb, strideB,
                                 batch, info, s),
                       "potrs launch");
-}
-
-template <typename F>
-batchlas_status guarded(F&& f) {
-    try {
-        return f();
-    } catch (const std::exception& e) {
-        return fail(BATCHLAS_INTERNAL, std::string("internal error: ") + e.what());
-    } catch (...) {
-        return fail(BATCHLAS_INTERNAL, "internal error");
-    }
 }
 
 }  // namespace
@@ -483,7 +443,7 @@ const char* batchlas_status_string(batchlas_status s) {
     return "unknown status";
 }
 
-const char* batchlas_last_error(void) { return g_last_error.c_str(); }
+const char* batchlas_last_error(void) { return bl::last_error(); }
 
 int32_t batchlas_version(void) { return 100; }
 
