@@ -1,4 +1,5 @@
-"""Python binding for libbatchlas (batched Cholesky potrf / posv on MI355X).
+"""Python binding for libbatchlas (batched Cholesky potrf / posv on MI355X, and
+the low-bit layer operators that such solves calibrate, in layer.py).
 
 Argument marshalling only: every step of the computation runs in the HIP
 kernels of libbatchlas.so, called through its C ABI (include/batchlas.h).
@@ -32,6 +33,8 @@ EXPORTS = [
     "batchlas_spotrf", "batchlas_dpotrf", "batchlas_cpotrf", "batchlas_zpotrf",
     "batchlas_sposv", "batchlas_dposv", "batchlas_cposv", "batchlas_zposv",
     "batchlas_route", "batchlas_status_string", "batchlas_last_error", "batchlas_version",
+    "batchlas_rmsnorm_quant", "batchlas_rmsnorm_grad", "batchlas_rmsnorm_grad_workspace",
+    "batchlas_weight_quant", "batchlas_weight_matvec",
 ]
 
 
@@ -87,8 +90,20 @@ def load_library():
                                              i64, vp, vp]
         lib.batchlas_route.argtypes = [i32, i32, i32, i64, i64, i64, i64, i64,
                                        ctypes.POINTER(RouteInfo)]
+        f64 = ctypes.c_double
+        lib.batchlas_rmsnorm_quant.argtypes = [i32, i32, i64, i64, vp, i64, vp, i64, vp, f64, vp, i64,
+                                               vp, i64, vp, i64, vp]
+        lib.batchlas_rmsnorm_grad.argtypes = [i32, i64, i64, vp, i64, vp, i64, vp, vp, i64, f64, vp,
+                                              i64, vp, vp, i64, vp]
+        lib.batchlas_rmsnorm_grad_workspace.argtypes = [i32, i64, i64, ctypes.POINTER(i64)]
+        lib.batchlas_weight_quant.argtypes = [i32, i32, i64, i64, i64, vp, i64, vp, i64, vp, i64, vp,
+                                              i64, vp, i64, vp]
+        lib.batchlas_weight_matvec.argtypes = [i32, i32, i32, i32, i64, i64, i64, i64, vp, i64, vp, i64,
+                                               vp, i64, vp, i64, vp, i64, vp, i64, vp]
         for name in ("batchlas_potrf", "batchlas_posv", "batchlas_potrf_family",
-                     "batchlas_posv_family", "batchlas_route"):
+                     "batchlas_posv_family", "batchlas_route", "batchlas_rmsnorm_quant",
+                     "batchlas_rmsnorm_grad", "batchlas_rmsnorm_grad_workspace",
+                     "batchlas_weight_quant", "batchlas_weight_matvec"):
             getattr(lib, name).restype = i32
         lib.batchlas_status_string.argtypes = [i32]
         lib.batchlas_status_string.restype = ctypes.c_char_p
@@ -207,3 +222,18 @@ def route(dtype: str, uplo: str, n: int, batch: int, nrhs: int = 0, family: str 
 
 def version() -> int:
     return load_library().batchlas_version()
+
+
+# ---------------------------------------------------------------- low-bit layer operators
+# In modules of their own, which import torch; loaded at first use.
+_LAZY = {"rmsnorm_quant": "layer", "rmsnorm_grad": "layer", "rmsnorm_grad_workspace": "layer",
+         "weight_quant": "layer", "weight_matvec": "layer"}
+
+
+def __getattr__(name: str):
+    if name in _LAZY:
+        import importlib
+        f = getattr(importlib.import_module("." + _LAZY[name], __name__), name)
+        globals()[name] = f
+        return f
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,0 +1,52 @@
+// Dispatch of the low-bit layer operators by element type (host only).
+#include "layer.hpp"
+
+namespace bl {
+
+#define BL_DECLARE_LAYER(suf)                                                                 \
+    hipError_t rmsnorm_quant_##suf(Scale sc, const NormQuantArgs& a, hipStream_t s);          \
+    hipError_t rmsnorm_grad_##suf(const NormGradArgs& a, hipStream_t s);                      \
+    int64_t rmsnorm_grad_partials_##suf(int64_t rows, int64_t n);                             \
+    hipError_t weight_quant_##suf(Format f, int group, const WeightQuantArgs& a, hipStream_t s);
+BL_DECLARE_LAYER(f32)
+BL_DECLARE_LAYER(f16)
+BL_DECLARE_LAYER(bf16)
+#undef BL_DECLARE_LAYER
+
+#define BL_BY_TYPE(call)                    \
+    switch (t) {                            \
+    case Type::F32: return call(f32);       \
+    case Type::F16: return call(f16);       \
+    case Type::BF16: return call(bf16);     \
+    case Type::E4M3: break;                 \
+    }
+
+hipError_t rmsnorm_quant(Type t, Scale sc, const NormQuantArgs& a, hipStream_t s) {
+#define BL_CALL(suf) rmsnorm_quant_##suf(sc, a, s)
+    BL_BY_TYPE(BL_CALL)
+#undef BL_CALL
+    return hipErrorInvalidValue;
+}
+
+hipError_t rmsnorm_grad(Type t, const NormGradArgs& a, hipStream_t s) {
+#define BL_CALL(suf) rmsnorm_grad_##suf(a, s)
+    BL_BY_TYPE(BL_CALL)
+#undef BL_CALL
+    return hipErrorInvalidValue;
+}
+
+int64_t rmsnorm_grad_partials(Type t, int64_t rows, int64_t n) {
+#define BL_CALL(suf) rmsnorm_grad_partials_##suf(rows, n)
+    BL_BY_TYPE(BL_CALL)
+#undef BL_CALL
+    return 0;
+}
+
+hipError_t weight_quant(Type t, Format f, int group, const WeightQuantArgs& a, hipStream_t s) {
+#define BL_CALL(suf) weight_quant_##suf(f, group, a, s)
+    BL_BY_TYPE(BL_CALL)
+#undef BL_CALL
+    return hipErrorInvalidValue;
+}
+
+}  // namespace bl

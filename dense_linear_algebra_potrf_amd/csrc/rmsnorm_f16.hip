@@ -1,0 +1,17 @@
+// RMS norm to 8 bits and its gradient for element type f16 (one translation
+// unit per type).
+#include "rmsnorm_impl.hpp"
+
+namespace bl {
+
+hipError_t rmsnorm_quant_f16(Scale sc, const NormQuantArgs& a, hipStream_t s) {
+    return rmsnorm_detail::rmsnorm_quant_t<layer::f16>(sc, a, s);
+}
+hipError_t rmsnorm_grad_f16(const NormGradArgs& a, hipStream_t s) {
+    return rmsnorm_detail::rmsnorm_grad_t<layer::f16>(a, s);
+}
+int64_t rmsnorm_grad_partials_f16(int64_t rows, int64_t n) {
+    return rmsnorm_detail::grad_partials(rows, n);
+}
+
+}  // namespace bl

@@ -1,0 +1,135 @@
+// Rounding of weights to 4-bit codes with group scales.
+//
+// A thread holds 8 neighbouring columns of a row (one dword of codes), so a
+// group of 32, 64 or 128 columns is held by 4, 8 or 16 neighbouring lanes of a
+// DPP row, and its largest magnitude (or least and largest value) takes two to
+// four lane exchanges.  One pass: W is read once, the codes and values written
+// once.
+#pragma once
+
+#include "layer_impl.hpp"
+
+namespace bl {
+namespace weight_quant_detail {
+
+using namespace layer;
+
+struct Least { __device__ __forceinline__ float operator()(float a, float b) const { return fminf(a, b); } };
+struct Most { __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); } };
+
+// The code of the e2m1 float next to t, |t| <= 6, ties to the even mantissa (0.25 -> 0, 0.75 -> 1, ..., 5 -> 4).
+__device__ __forceinline__ uint32_t e2m1_code(float t) {
+    const float v = fabsf(t);
+    const float steps = v < 2.0f ? rintf(v * 2.0f)            // 0, 0.5, 1, 1.5, (2): codes 0..4
+                        : v < 4.0f ? rintf(v) + 2.0f          // 2, 3, (4): codes 4..6
+                                   : rintf(v * 0.5f) + 4.0f;  // 4, 6: codes 6, 7
+    return uint32_t(steps) | (__builtin_bit_cast(uint32_t, t) >> 28 & 8u);
+}
+__device__ __forceinline__ float e2m1_value(uint32_t code) {
+    const uint32_t c = code & 7;
+    // exponent field c / 2 (bias 1), one mantissa bit; 0 and 1 are subnormal
+    const float v = c < 2 ? 0.5f * float(c) : __builtin_bit_cast(float, (126 + (c >> 1)) << 23 | (c & 1) << 22);
+    return code & 8 ? -v : v;
+}
+
+template <typename T, Format F, int GROUP, bool ZEROS>
+__global__ __launch_bounds__(256) void weight_quant_kernel(WeightQuantArgs a) {
+    constexpr int LANES = GROUP / 8;
+    const int64_t per_row = (a.k + 127) / 128 * 16;           // threads of a row: whole DPP rows
+    const int64_t total = a.n * per_row;
+    for (int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x; id < total; id += int64_t(gridDim.x) * 256) {
+        const int64_t row = id / per_row;
+        const int c = int(id - row * per_row) * 8;
+        const int left = int(a.k) - c;
+        const Raw8<T> wr = load8(static_cast<const T*>(a.W) + row * a.ldw + c, left);
+        float w[8], value[8];
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            w[j] = wr[j];
+            top = Max{}(top, magnitude(w[j]));
+        }
+        top = row_reduce<LANES>(top, Max{});
+        bool finite = top < kInfBits;
+        uint32_t codes = 0;
+        const int64_t g = c / GROUP;
+        const bool head = (threadIdx.x & (LANES - 1)) == 0 && left > 0;
+        if constexpr (F == Format::FLOAT) {
+            const uint32_t b = e2m1_scale_byte(top);
+            const float up = power_of(b), down = power_of(b == 255 ? 255 : 254 - b);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t u = finite ? e2m1_code(w[j] * down) : 0;
+                codes |= u << (4 * j);
+                value[j] = e2m1_value(u) * up;
+            }
+            if (head) static_cast<uint8_t*>(a.scales)[row * a.lds + g] = uint8_t(b);
+        } else {
+            float span, z = 8;
+            [[maybe_unused]] float least = 0;
+            if constexpr (ZEROS) {
+                float most = 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    least = fminf(least, w[j]);
+                    most = fmaxf(most, w[j]);
+                }
+                least = row_reduce<LANES>(least, Least{});
+                most = row_reduce<LANES>(most, Most{});
+                span = (most - least) / 15.0f;
+                finite = finite && magnitude(span) < kInfBits;
+            } else {
+                span = __builtin_bit_cast(float, top) / 7.0f;
+            }
+            const bf16 stored = bf16(finite ? fmaxf(float(bf16(span)), kTiny) : __builtin_nanf(""));
+            const float scale = float(stored);
+            if constexpr (ZEROS)
+                if (finite) z = fminf(fmaxf(rintf(-least / scale), 0.0f), 15.0f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float q = ZEROS ? fminf(fmaxf(rintf(w[j] / scale) + z, 0.0f), 15.0f)
+                                      : fminf(fmaxf(rintf(w[j] / scale), -8.0f), 7.0f) + 8.0f;
+                codes |= (finite ? uint32_t(q) : 0u) << (4 * j);
+                value[j] = (q - z) * scale;
+            }
+            if (head) {
+                static_cast<bf16*>(a.scales)[row * a.lds + g] = stored;
+                if constexpr (ZEROS) a.zeros[row * a.ldz + g] = uint8_t(z);
+            }
+        }
+        if (left <= 0) continue;
+        if (left < 8) codes &= (1u << (4 * left)) - 1;         // the half byte past an odd k
+        uint8_t* out = a.codes + row * a.ldc + c / 2;
+        if (left >= 7) {
+            *reinterpret_cast<uint32_t*>(out) = codes;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 3; ++j)
+                if (2 * j < left) out[j] = uint8_t(codes >> (8 * j));
+        }
+        if (a.values) store8(static_cast<T*>(a.values) + row * a.ldv + c, value, left);
+    }
+}
+
+template <typename T>
+inline hipError_t weight_quant_t(Format f, int group, const WeightQuantArgs& a, hipStream_t s) {
+    const int64_t need = (a.n * ((a.k + 127) / 128 * 16) + 255) / 256;
+    const int64_t most = 1 << 20;
+    const dim3 grid(uint32_t(need < most ? need : most)), block(256);
+    auto go = [&](auto fmt, auto size, auto zeros) {
+        return launch(weight_quant_kernel<T, decltype(fmt)::value, decltype(size)::value, decltype(zeros)::value>,
+                      grid, block, 0, s, a);
+    };
+    using I = std::integral_constant<Format, Format::INTEGER>;
+    if (f == Format::FLOAT) return go(std::integral_constant<Format, Format::FLOAT>{}, ic<32>{}, std::false_type{});
+    if (a.zeros)
+        return group == 32   ? go(I{}, ic<32>{}, std::true_type{})
+               : group == 64 ? go(I{}, ic<64>{}, std::true_type{})
+                             : go(I{}, ic<128>{}, std::true_type{});
+    return group == 32   ? go(I{}, ic<32>{}, std::false_type{})
+           : group == 64 ? go(I{}, ic<64>{}, std::false_type{})
+                         : go(I{}, ic<128>{}, std::false_type{});
+}
+
+}  // namespace weight_quant_detail
+}  // namespace bl

@@ -1,7 +1,8 @@
 /*
  * batchlas -- batched Cholesky factorisation (potrf) and positive-definite
  * solve (posv) for many small independent Hermitian positive-definite
- * matrices, on AMD Instinct MI355X (gfx950).
+ * matrices, on AMD Instinct MI355X (gfx950), and the operators of layers whose
+ * 4-bit weights those solves calibrate ("Low-bit layer operators" below).
  *
  * The operations are the ones described on the BatchLAS documentation's
  * perf_potrf page:
@@ -14,8 +15,8 @@
  * Per-matrix failure is reported through info, with the first failing
  * column winning (section "potrf: correctness findings", item 6).
  *
- * Conventions shared by every entry point
- * ---------------------------------------
+ * Conventions shared by the potrf and posv entry points
+ * -----------------------------------------------------
  * Memory   All array pointers are DEVICE pointers owned by the caller.  The
  *          library allocates nothing persistent, keeps no pointer after it
  *          returns and makes no host<->device copy of its own.
@@ -71,8 +72,8 @@ typedef enum {
 
 typedef enum {
     BATCHLAS_OK = 0,
-    BATCHLAS_INVALID_VALUE = 1,   /* a size, leading dimension, stride, dtype or uplo is out of range */
-    BATCHLAS_NULL_POINTER = 2,    /* A (or B) is NULL                                               */
+    BATCHLAS_INVALID_VALUE = 1,   /* a size, leading dimension, stride, dtype, uplo or alignment is out of range */
+    BATCHLAS_NULL_POINTER = 2,    /* A (or B, or an operator's array) is NULL                        */
     BATCHLAS_NOT_SUPPORTED = 3,   /* no kernel family serves this shape / the pinned family cannot   */
     BATCHLAS_HIP_ERROR = 4,       /* the HIP runtime reported an error while enqueueing              */
     BATCHLAS_INTERNAL = 5         /* an internal invariant failed                                    */
@@ -190,6 +191,147 @@ batchlas_status batchlas_zposv(batchlas_uplo uplo, int64_t n, int64_t nrhs, void
 batchlas_status batchlas_route(batchlas_family family, batchlas_dtype dt, batchlas_uplo uplo,
                                int64_t n, int64_t nrhs, int64_t lda, int64_t strideA,
                                int64_t batch, batchlas_route_info *out);
+
+/*
+ * Low-bit layer operators
+ * -----------------------
+ * What a layer with 4-bit weights runs beside the solves that calibrate it: the
+ * weights' rounding in groups (its error is pushed onto the columns not yet
+ * rounded by a positive-definite solve), products of a few tokens with such
+ * weights, and the root-mean-square norm that writes their activations in 8
+ * bits, with its gradient.
+ *
+ * Layout   Matrices here are ROW-major: element (i, c) of x is x[i * ldx + c]
+ *          with ldx >= the row's length, in elements.  Rows may start at any
+ *          address that is a multiple of the element size, except for codes.
+ * Memory   Device pointers owned by the caller, as above.  Buffers do not
+ *          overlap, except that h of rmsnorm_quant may be x or r itself, and
+ *          dx of rmsnorm_grad may be dy, h or dh itself (same leading
+ *          dimension).
+ * Empty    rows (m) may be 0: nothing is computed (dw is set to zero).
+ * Errors   Checked synchronously, before anything is enqueued and with no
+ *          writes, in this order: types, formats and group; sizes; leading
+ *          dimensions; non-null pointers; alignment; the shape supported.
+ * Streams  As above.  Every operator gives the same bits on every run, and can
+ *          be captured in a graph.
+ *
+ * 8-bit values are e4m3 floats (1 sign, 4 exponent, 3 mantissa bits, bias 7, no
+ * infinity, 0x7f is NaN, largest 448).  Their scales are either one per row (a
+ * float) or one per block of 32 columns (a byte b meaning 2^(b - 127), 255
+ * meaning NaN; the last block of a row may be shorter).  A value is its e4m3
+ * float times its scale.
+ *
+ * 4-bit weights are codes, two to a byte, column c of a row in byte c / 2, even
+ * columns in the low four bits.  Rows of codes are held in whole 16 bytes,
+ * which weight_matvec reads (the padding may hold anything): codes and ldc (in
+ * bytes, >= (k + 1) / 2) are multiples of 16.  Each group of `group` columns has a scale (the last group of a row may be shorter):
+ *   INTEGER  code u in 0..15 is (u - z) * scale, scale in bf16, z the group's
+ *            byte in `zeros` (0..15), 8 where zeros is NULL; group 32, 64 or 128
+ *   FLOAT    code is an e2m1 float (1 sign bit, then 0 0.5 1 1.5 2 3 4 6) times
+ *            scale, a byte b meaning 2^(b - 127), 255 meaning NaN; group 32
+ */
+typedef enum {
+    BATCHLAS_TYPE_F32 = 0,    /* float                          */
+    BATCHLAS_TYPE_F16 = 1,    /* half                           */
+    BATCHLAS_TYPE_BF16 = 2,   /* bfloat16                       */
+    BATCHLAS_TYPE_E4M3 = 3    /* 8-bit float, only with scales  */
+} batchlas_type;
+
+typedef enum {
+    BATCHLAS_SCALE_NONE = 0,
+    BATCHLAS_SCALE_ROW = 1,     /* float[rows]                                    */
+    BATCHLAS_SCALE_BLOCK = 2    /* a byte per 32 columns, row stride in bytes     */
+} batchlas_scale;
+
+typedef enum {
+    BATCHLAS_FORMAT_INTEGER = 0,
+    BATCHLAS_FORMAT_FLOAT = 1
+} batchlas_format;
+
+/*
+ * rmsnorm_quant: for every row,
+ *   h = x + r,   v = w * h / sqrt(mean(h^2) + eps),   q = e4m3(v / scale)
+ * in 32 bits; v comes from h before h is rounded to the type.
+ *   type     F32, F16 or BF16: of x, r, w and h
+ *   scale    ROW: scales[i] = max(max|v| / 448, 2^-126), a float;
+ *            BLOCK: 2^e with the least e in -127..127 for which
+ *            max|v| <= 448 * 2^e, a byte e + 127, at scales[i * lds + block]
+ *   r        NULL: no residual, and h must be NULL
+ *   h        receives x + r, rounded to the type; NULL: not stored
+ *   eps      >= 0
+ *   lds      >= (n + 31) / 32 for BLOCK; not read for ROW
+ * A row (block) that holds a v that is not finite gets a NaN scale and NaN
+ * values; a row of zeros gets the smallest scale and zeros.
+ * n is at most 32768, else NOT_SUPPORTED.
+ */
+batchlas_status batchlas_rmsnorm_quant(batchlas_type type, batchlas_scale scale, int64_t rows,
+                                       int64_t n, const void *x, int64_t ldx, const void *r,
+                                       int64_t ldr, const void *w, double eps, void *h,
+                                       int64_t ldh, uint8_t *q, int64_t ldq, void *scales,
+                                       int64_t lds, batchlas_stream_t stream);
+
+/*
+ * rmsnorm_grad: the gradient of the norm at the stored h.  With
+ * s = 1 / sqrt(mean(h^2) + eps), and dy the gradient of v,
+ *   dx = dh + s * (dy * w - h * s^2 * mean(dy * w * h))      (of x and of r)
+ *   dw = sum over rows of dy * h * s                         (float[n])
+ *   dh       the gradient that reaches h on the residual path; NULL: zero
+ *   dw       NULL: not computed
+ *   workspace  device memory of at least the bytes that
+ *            batchlas_rmsnorm_grad_workspace gives, aligned to 4 bytes; not
+ *            used (may be NULL) where that is 0 or dw is NULL
+ * n is at most 16384, else NOT_SUPPORTED.
+ */
+batchlas_status batchlas_rmsnorm_grad(batchlas_type type, int64_t rows, int64_t n, const void *dy,
+                                      int64_t lddy, const void *h, int64_t ldh, const void *w,
+                                      const void *dh, int64_t lddh, double eps, void *dx,
+                                      int64_t lddx, float *dw, void *workspace,
+                                      int64_t workspace_bytes, batchlas_stream_t stream);
+
+/* Host-only: the workspace that rmsnorm_grad of this size needs, in bytes. */
+batchlas_status batchlas_rmsnorm_grad_workspace(batchlas_type type, int64_t rows, int64_t n,
+                                                int64_t *bytes);
+
+/*
+ * weight_quant: rounds the rows of W (n x k) to 4 bits.  Per group of columns:
+ *   INTEGER, zeros NULL:  scale = max(bf16(max|w| / 7), 2^-126),
+ *       u = clamp(rint(w / scale), -8, 7) + 8
+ *   INTEGER, zeros given: lo = min(w, 0), hi = max(w, 0),
+ *       scale = max(bf16((hi - lo) / 15), 2^-126),
+ *       z = clamp(rint(-lo / scale), 0, 15), u = clamp(rint(w / scale) + z, 0, 15)
+ *   FLOAT: scale 2^e with the least e in -127..127 for which
+ *       max|w| <= 6 * 2^e, code = e2m1(w / scale)
+ * Every rounding is to nearest, ties to even; quotients are rounded to 32 bits.
+ *   type     F32, F16 or BF16: of W and of values
+ *   scales   bf16 (INTEGER) or bytes (FLOAT), group g of row i at
+ *            scales[i * lds + g]; zeros likewise with ldz, NULL for FLOAT
+ *   values   receives what the codes stand for, rounded to the type; NULL: not
+ *            stored
+ * A group that holds a weight that is not finite, or whose hi - lo overflows,
+ * gets a NaN scale, codes of zero (and z = 8) and NaN values.  The unused half byte of an odd k is a code
+ * of zero; bytes beyond (k + 1) / 2 of a row are not written.
+ */
+batchlas_status batchlas_weight_quant(batchlas_type type, batchlas_format format, int64_t group,
+                                      int64_t n, int64_t k, const void *W, int64_t ldw,
+                                      uint8_t *codes, int64_t ldc, void *scales, int64_t lds,
+                                      uint8_t *zeros, int64_t ldz, void *values, int64_t ldv,
+                                      batchlas_stream_t stream);
+
+/*
+ * weight_matvec: y = x W^T, y (m x n), x (m x k), W (n x k) held as codes, sums
+ * in 32 bits.  Made for the few rows of a decoding step (m up to about 64);
+ * any m up to 2^21 is computed, reading W once per 64 rows.
+ *   xtype, xscale   F16 or BF16 with NONE, or E4M3 with ROW (xscales float[m])
+ *            or BLOCK (bytes, row stride ldxs >= (k + 31) / 32)
+ *   ytype    F32, F16 or BF16
+ */
+batchlas_status batchlas_weight_matvec(batchlas_type xtype, batchlas_scale xscale,
+                                       batchlas_type ytype, batchlas_format format, int64_t group,
+                                       int64_t m, int64_t n, int64_t k, const void *x,
+                                       int64_t ldx, const void *xscales, int64_t ldxs,
+                                       const uint8_t *codes, int64_t ldc, const void *scales,
+                                       int64_t lds, const uint8_t *zeros, int64_t ldz, void *y,
+                                       int64_t ldy, batchlas_stream_t stream);
 
 /* Static text for a status code. */
 const char *batchlas_status_string(batchlas_status s);

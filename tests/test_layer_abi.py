@@ -1,0 +1,199 @@
+"""The low-bit layer operators without a GPU: refusals in the documented order
+before anything touches the GPU, the empty calls, the workspace query, the
+binding's own checks, and the 64-bit formulas the GPU tests compare against
+(the gradient against differences)."""
+from __future__ import annotations
+
+import ctypes
+import os
+
+import numpy as np
+import pytest
+
+import dense_linear_algebra_potrf_amd as bl
+from dense_linear_algebra_potrf_amd import build as blbuild
+from tests import _layer_ref as ref
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(bl.LIB_PATH):
+        blbuild.build(incremental=True, verbose=False)
+    return bl.load_library()
+
+
+P = 0x1000     # never dereferenced: validation fails first
+
+
+def call(lib, name, defaults, order, over):
+    a = dict(defaults, **over)
+    st = getattr(lib, "batchlas_" + name)(*[a[k] for k in order])
+    return st, lib.batchlas_last_error().decode()
+
+
+QUANT = dict(type=2, scale=2, rows=4, n=64, x=P, ldx=64, r=P, ldr=64, w=P, eps=1e-6, h=P, ldh=64, q=P, ldq=64,
+             scales=P, lds=2, stream=None)
+
+
+@pytest.mark.parametrize("over,status,msg", [
+    (dict(type=3), 1, "type must be"), (dict(type=-1), 1, "type must be"), (dict(scale=0), 1, "scale must be"),
+    (dict(rows=-1), 1, "rows must be"), (dict(n=0), 1, "n must be"), (dict(rows=1 << 31), 1, "out of range"),
+    (dict(eps=-1.0), 1, "eps must be"), (dict(eps=float("nan")), 1, "eps must be"),
+    (dict(ldx=63), 1, "ldx must be"), (dict(ldr=63), 1, "ldr must be"), (dict(ldh=63), 1, "ldh must be"),
+    (dict(ldq=63), 1, "ldq must be"), (dict(lds=1), 1, "lds must be"), (dict(ldx=1 << 60), 1, "overflows"),
+    (dict(r=None), 1, "needs a residual"), (dict(x=None), 2, "x is NULL"), (dict(w=None), 2, "w is NULL"),
+    (dict(q=None), 2, "q is NULL"), (dict(scales=None), 2, "scales is NULL"), (dict(x=P + 1), 1, "not aligned"),
+    (dict(scale=1, scales=P + 2), 1, "not aligned"),
+    (dict(n=32769, ldx=32769, ldr=32769, ldh=32769, ldq=32769, lds=1025), 3, "at most"),
+    (dict(type=9, n=0, x=None), 1, "type must be"), (dict(n=0, ldx=0, x=None), 1, "n must be"),
+    (dict(rows=0, x=None, w=None, q=None, scales=None), 0, ""),
+])
+def test_rmsnorm_quant_refusals(lib, over, status, msg):
+    st, text = call(lib, "rmsnorm_quant", QUANT, list(QUANT), over)
+    assert st == status
+    assert msg in text
+
+
+GRAD = dict(type=0, rows=4, n=64, dy=P, lddy=64, h=P, ldh=64, w=P, dh=P, lddh=64, eps=1e-6, dx=P, lddx=64, dw=P,
+            workspace=P, bytes=1 << 30, stream=None)
+
+
+@pytest.mark.parametrize("over,status,msg", [
+    (dict(type=3), 1, "type must be"), (dict(rows=-1), 1, "rows must be"), (dict(n=0), 1, "n must be"),
+    (dict(eps=-1e-9), 1, "eps must be"), (dict(lddy=3), 1, "lddy must be"), (dict(ldh=3), 1, "ldh must be"),
+    (dict(lddh=3), 1, "lddh must be"), (dict(lddx=3), 1, "lddx must be"), (dict(dy=None), 2, "dy is NULL"),
+    (dict(h=None), 2, "h is NULL"), (dict(w=None), 2, "w is NULL"), (dict(dx=None), 2, "dx is NULL"),
+    (dict(dw=P + 2), 1, "not aligned"), (dict(workspace=None), 2, "workspace is NULL"),
+    (dict(bytes=16), 1, "workspace_bytes"), (dict(n=16385, lddy=16385, ldh=16385, lddh=16385, lddx=16385), 3,
+                                             "at most"),
+    (dict(rows=0, dw=None, dy=None, h=None, w=None, dx=None), 0, ""),
+])
+def test_rmsnorm_grad_refusals(lib, over, status, msg):
+    st, text = call(lib, "rmsnorm_grad", GRAD, list(GRAD), over)
+    assert st == status
+    assert msg in text
+
+
+def test_rmsnorm_grad_workspace(lib):
+    size = ctypes.c_int64(-1)
+    assert lib.batchlas_rmsnorm_grad_workspace(2, 0, 100, ctypes.byref(size)) == 0 and size.value == 0
+    assert lib.batchlas_rmsnorm_grad_workspace(2, 1, 100, ctypes.byref(size)) == 0 and size.value == 0
+    for rows, n in ((2, 1), (517, 1537), (1 << 20, 4096), (3, 16384)):
+        assert lib.batchlas_rmsnorm_grad_workspace(1, rows, n, ctypes.byref(size)) == 0
+        assert size.value % (4 * n) == 0 and 4 * n <= size.value <= 4 * n * min(4 * rows, 4096)
+    assert lib.batchlas_rmsnorm_grad_workspace(1, 4, 16385, ctypes.byref(size)) == 3
+    assert lib.batchlas_rmsnorm_grad_workspace(3, 4, 64, ctypes.byref(size)) == 1
+    assert lib.batchlas_rmsnorm_grad_workspace(1, 4, 64, None) == 2
+
+
+WQ = dict(type=0, format=0, group=64, n=4, k=100, W=P, ldw=100, codes=P, ldc=64, scales=P, lds=2, zeros=P, ldz=2,
+          values=P, ldv=100, stream=None)
+
+
+@pytest.mark.parametrize("over,status,msg", [
+    (dict(type=3), 1, "type must be"), (dict(format=2), 1, "unknown format"), (dict(group=16), 1, "group must be"),
+    (dict(group=96), 1, "group must be"), (dict(format=1, group=64), 1, "group must be 32"), (dict(n=0), 1, "n must be"),
+    (dict(k=0), 1, "k must be"), (dict(k=1 << 31, ldw=1 << 31), 1, "out of range"), (dict(ldw=99), 1, "ldw must be"),
+    (dict(ldv=99), 1, "ldv must be"), (dict(ldc=48), 1, "ldc must be >="), (dict(ldc=56), 1, "multiple of 16"),
+    (dict(lds=1), 1, "lds must be"), (dict(ldz=1), 1, "ldz must be"),
+    (dict(format=1, group=32, lds=4, ldz=4), 1, "has no zeros"), (dict(W=None), 2, "W is NULL"),
+    (dict(codes=None), 2, "codes is NULL"), (dict(scales=None), 2, "scales is NULL"),
+    (dict(codes=P + 8), 1, "aligned to 16"), (dict(W=P + 2), 1, "not aligned"), (dict(scales=P + 1), 1, "not aligned"),
+    (dict(ldw=1 << 60), 1, "overflows"),
+])
+def test_weight_quant_refusals(lib, over, status, msg):
+    st, text = call(lib, "weight_quant", WQ, list(WQ), over)
+    assert st == status
+    assert msg in text
+
+
+MV = dict(xtype=3, xscale=2, ytype=2, format=0, group=32, m=2, n=4, k=100, x=P, ldx=100, xscales=P, ldxs=4, codes=P,
+          ldc=64, scales=P, lds=4, zeros=P, ldz=4, y=P, ldy=4, stream=None)
+
+
+@pytest.mark.parametrize("over,status,msg", [
+    (dict(xtype=0), 1, "xtype must be"), (dict(xscale=0), 1, "xscale must be"), (dict(xtype=2), 1, "xscale must be"),
+    (dict(ytype=3), 1, "ytype must be"), (dict(format=7), 1, "unknown format"), (dict(group=0), 1, "group must be"),
+    (dict(m=-1), 1, "m must be"), (dict(n=0), 1, "n must be"), (dict(k=0), 1, "k must be"),
+    (dict(ldx=99), 1, "ldx must be"), (dict(ldxs=3), 1, "ldxs must be"), (dict(ldc=49), 1, "ldc must be >="),
+    (dict(lds=3), 1, "lds must be"), (dict(ldz=3), 1, "ldz must be"), (dict(ldy=3), 1, "ldy must be"),
+    (dict(format=1), 1, "has no zeros"), (dict(x=None), 2, "x is NULL"), (dict(xscales=None), 2, "xscales is NULL"),
+    (dict(codes=None), 2, "codes is NULL"), (dict(scales=None), 2, "scales is NULL"), (dict(y=None), 2, "y is NULL"),
+    (dict(codes=P + 4), 1, "aligned to 16"), (dict(y=P + 1), 1, "not aligned"),
+    (dict(xscale=1, xscales=P + 2), 1, "not aligned"), (dict(m=(1 << 21) + 1), 3, "m is beyond"),
+    (dict(n=(1 << 24) + 1, ldy=1 << 25), 3, "n is beyond"), (dict(m=0, x=None, y=None, codes=None), 0, ""),
+])
+def test_weight_matvec_refusals(lib, over, status, msg):
+    if over.get("ldc") == 49:
+        over = dict(over, ldc=48)
+    st, text = call(lib, "weight_matvec", MV, list(MV), over)
+    assert st == status
+    assert msg in text
+
+
+def test_binding_refuses_host_tensors_and_wrong_types(lib):
+    import torch
+    x = torch.zeros(2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="GPU"):
+        bl.rmsnorm_quant(x, x[0])
+    with pytest.raises(TypeError, match="float32, float16 or bfloat16"):
+        bl.rmsnorm_quant(x.double(), x[0])
+    with pytest.raises(ValueError, match="GPU"):
+        bl.rmsnorm_grad(x, x, x[0])
+    with pytest.raises(ValueError, match="GPU"):
+        bl.weight_quant(x)
+    with pytest.raises(TypeError, match="x must be"):
+        bl.weight_matvec(x.float(), x, x)
+    with pytest.raises(AttributeError):
+        bl.no_such_operator
+
+
+# ---------------------------------------------------------------- the formulas themselves
+
+@pytest.mark.parametrize("n,with_dh", [(1, False), (5, True), (33, False)])
+def test_gradient_formula_against_differences(n, with_dh):
+    """d/dh of sum(dy v) + sum(dh h), by central differences in 64 bits: step
+    1e-5 leaves a truncation error near 1e-10 and a rounding error near 1e-11."""
+    rng = np.random.default_rng(n)
+    h, dy, dh, w = (rng.standard_normal((3, n)) for _ in range(4))
+    w = 1 + 0.2 * w[0]
+    dh = dh if with_dh else None
+    loss = lambda h_, w_: (dy * ref.norm(h_, w_, 1e-6)).sum() + (0 if dh is None else (dh * h_).sum())  # noqa: E731
+    dx, dw = ref.norm_grad(dy, h, w, dh, 1e-6)
+    step = 1e-5
+    for i in range(3):
+        for c in range(n):
+            d = np.zeros_like(h)
+            d[i, c] = step
+            assert abs((loss(h + d, w) - loss(h - d, w)) / (2 * step) - dx[i, c]) <= 1e-7
+    for c in range(n):
+        d = np.zeros(n)
+        d[c] = step
+        assert abs((loss(h, w + d) - loss(h, w - d)) / (2 * step) - dw[c]) <= 1e-7
+
+
+def test_reference_rounding_to_four_bits():
+    """Hand-worked groups: exact grids, ties to even, zero points, empty and broken groups."""
+    w = np.zeros((1, 32), np.float32)
+    w[0, :8] = [6, -6, 0.25, 0.75, 1.25, 2.5, 3.5, -5]
+    code, scale, _, val = ref.quant(w, "fp4", 32, False)
+    assert scale[0, 0] == 1 and list(val[0, :8]) == [6, -6, 0, 1, 1, 2, 4, -4]
+    assert list(code[0, :8]) == [7, 15, 0, 2, 2, 4, 6, 14]
+    assert ref.quant(w * 2 ** -20, "fp4", 32, False)[1][0, 0] == 2.0 ** -20
+    assert ref.quant(np.full((1, 32), 6.1, np.float32), "fp4", 32, False)[1][0, 0] == 2
+    w[0, :4] = [7, -7, 0.5, 1.5]
+    code, scale, _, val = ref.quant(w, "int4", 32, False)
+    assert scale[0, 0] == 1 and list(val[0, :4]) == [7, -7, 0, 2] and code[0, 31] == 8
+    w[:] = 0
+    w[0, :3] = [-5, 10, 0.5]
+    code, scale, z, val = ref.quant(w, "int4", 32, True)
+    assert scale[0, 0] == 1 and z[0, 0] == 5 and list(code[0, :4]) == [0, 15, 5, 5] and list(val[0, :3]) == [-5, 10, 0]
+    code, scale, z, val = ref.quant(np.zeros((1, 3), np.float32), "int4", 32, True)
+    assert scale[0, 0] == ref.TINY and z[0, 0] == 0 and not code.any() and not val.any()
+    w[0, 1] = np.inf
+    for fmt, zeros in (("int4", False), ("int4", True), ("fp4", False)):
+        code, scale, _, val = ref.quant(w, fmt, 32, zeros)
+        assert np.isnan(scale).all() and np.isnan(val).all() and not code.any()
+    packed = ref.pack(np.arange(5)[None])
+    assert list(packed[0, :3]) == [0x10, 0x32, 0x04] and packed.shape == (1, 16)
+    assert list(ref.unpack(packed, 5)[0]) == [0, 1, 2, 3, 4]
