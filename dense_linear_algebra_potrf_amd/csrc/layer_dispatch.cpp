@@ -49,4 +49,19 @@ hipError_t weight_quant(Type t, Format f, int group, const WeightQuantArgs& a, h
     return hipErrorInvalidValue;
 }
 
+#define BL_DECLARE_MATVEC(suf) \
+    hipError_t weight_matvec_##suf(Type yt, Format f, int group, const MatvecArgs& a, hipStream_t s);
+BL_DECLARE_MATVEC(bf16)
+BL_DECLARE_MATVEC(f16)
+BL_DECLARE_MATVEC(f8block)
+BL_DECLARE_MATVEC(f8row)
+#undef BL_DECLARE_MATVEC
+
+hipError_t weight_matvec(Type xt, Scale xs, Type yt, Format f, int group, const MatvecArgs& a, hipStream_t s) {
+    if (xt == Type::BF16) return weight_matvec_bf16(yt, f, group, a, s);
+    if (xt == Type::F16) return weight_matvec_f16(yt, f, group, a, s);
+    if (xs == Scale::BLOCK) return weight_matvec_f8block(yt, f, group, a, s);
+    return weight_matvec_f8row(yt, f, group, a, s);
+}
+
 }  // namespace bl
