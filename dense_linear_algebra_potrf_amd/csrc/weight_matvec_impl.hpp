@@ -46,6 +46,7 @@ constexpr bool is_eight(X x) { return x == X::F8_BLOCK || x == X::F8_ROW; }
 
 constexpr int kChunk = 128;       // columns a wavefront takes at a time
 constexpr int kWaves = 8;         // wavefronts of a workgroup, at most
+constexpr int kGroups = 256;      // groups of a row whose scales are in LDS at a time
 
 // Eight columns of a row as the matrix cores take them: words of two 16-bit floats.
 struct Frag { uint32_t word[4]; };
@@ -104,14 +105,8 @@ __device__ __forceinline__ Frag unpack(uint32_t w, [[maybe_unused]] f16x2 zero) 
     return f;
 }
 
-// What a lane reads of a chunk: the codes and scales of its rows of W,
-template <int GROUPS, int NB>
-struct Codes {
-    uint32_t codes[NB][4];
-    uint16_t scale[NB][GROUPS];
-    uint8_t zero[NB][GROUPS];
-};
-// and 8 columns of its rows of x for each of the chunk's four products.
+// What a lane holds of x for a chunk: 8 columns of its rows for each of the
+// chunk's four products.
 template <X XT, int MB>
 struct Rows {
     uint32_t x[MB][4][is_eight(XT) ? 2 : 4];
@@ -148,12 +143,15 @@ __global__ __launch_bounds__(64 * kWaves) void weight_matvec_kernel(MatvecArgs a
     constexpr bool HALF = in_half(XT), EIGHT = is_eight(XT);
     constexpr bool OFFSET = F == Format::INTEGER && !HALF;      // zero points are taken off the sums
     constexpr int GROUPS = kChunk / GROUP, STEPS = GROUP / 32;  // groups of a chunk, products of a group
-    using C = Codes<GROUPS, NB>;
-    __shared__ float sums[kWaves][MB * NB * 4][64];
+    constexpr int TILE = 16 * NB;                               // rows of W
+    __shared__ union {
+        uint32_t scales[kGroups][TILE];                         // of the groups at hand, as `scale_of` reads them
+        float sums[kWaves][MB * NB * 4][64];
+    } lds;
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
     const int r = lane & 15, g = lane >> 4;
-    const int64_t n0 = int64_t(blockIdx.x) * (16 * NB), m0 = int64_t(blockIdx.y) * (16 * MB);
+    const int64_t n0 = int64_t(blockIdx.x) * TILE, m0 = int64_t(blockIdx.y) * (16 * MB);
     const int64_t chunks = (a.k + kChunk - 1) / kChunk, whole = a.k / kChunk;
     const int64_t groups = (a.k + GROUP - 1) / GROUP;
 
@@ -164,46 +162,57 @@ __global__ __launch_bounds__(64 * kWaves) void weight_matvec_kernel(MatvecArgs a
 #pragma unroll
     for (int i = 0; i < MB; ++i) row_m[i] = m0 + 16 * i + r < a.m ? m0 + 16 * i + r : a.m - 1;
 
+    // Scales of the groups from `first` on, to LDS: a float's upper half and, for
+    // integers, the zero point in the lower.  Neighbouring lanes take neighbouring
+    // rows and 8 groups each, so that the writes spread over the banks.  Groups
+    // that the last chunk lacks get a finite scale; their products are zero.
+    auto stage = [&](int64_t first, int count) {
+        const int rounded = (count + GROUPS - 1) / GROUPS * GROUPS, octets = (rounded + 7) / 8;
+        for (int e = threadIdx.x; e < octets * TILE; e += blockDim.x) {
+            const int row = e % TILE, at = e / TILE * 8, left = count - at;
+            const int64_t n = n0 + row < a.n ? n0 + row : a.n - 1, s0 = n * a.lds + first + at;
+            uint32_t v[8];
+            if constexpr (F == Format::FLOAT) {
+                const uint8_t* p = static_cast<const uint8_t*>(a.scales) + s0;
+                uint8_t s[8] = {};
+                if (left >= 8) __builtin_memcpy(s, p, 8);
+                else
+                    for (int j = 0; j < 7; ++j) s[j] = j < left ? p[j] : 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = __builtin_bit_cast(uint32_t, power_of(s[j]));
+            } else {
+                const uint16_t* p = static_cast<const uint16_t*>(a.scales) + s0;
+                const uint8_t* q = a.zeros + n * a.ldz + first + at;
+                uint16_t s[8] = {};
+                uint8_t z[8] = {8, 8, 8, 8, 8, 8, 8, 8};
+                if (left >= 8) {
+                    __builtin_memcpy(s, p, 16);
+                    if (a.zeros) __builtin_memcpy(z, q, 8);
+                } else {
+                    for (int j = 0; j < 7; ++j) {
+                        s[j] = j < left ? p[j] : 0;
+                        if (a.zeros) z[j] = j < left ? q[j] : 0;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = uint32_t(s[j]) << 16 | z[j];
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (at + j < rounded) lds.scales[at + j][row] = v[j];
+        }
+    };
+
     // TAIL: the last chunk, which ends inside; what is past the row's end is zero.
-    auto load = [&](auto tail, int64_t c, C& d) {
-        constexpr bool TAIL = decltype(tail)::value;
+    auto load = [&](auto tail, int64_t c, uint32_t (&d)[NB][4]) {
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
             const int64_t at = c * (kChunk / 2) + 16 * g;
             u32x4 w = {0, 0, 0, 0};
-            if (!TAIL || at < (a.k + 1) / 2) w = *reinterpret_cast<const u32x4*>(a.codes + row_n[i] * a.ldc + at);
+            if (!decltype(tail)::value || at < (a.k + 1) / 2)
+                w = *reinterpret_cast<const u32x4*>(a.codes + row_n[i] * a.ldc + at);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) d.codes[i][j] = w[j];
-            const int64_t g0 = c * GROUPS, s0 = row_n[i] * a.lds + g0;
-            if constexpr (F == Format::FLOAT) {
-                uint8_t s[GROUPS] = {};
-                if (!TAIL || g0 + GROUPS <= groups) {
-                    __builtin_memcpy(s, static_cast<const uint8_t*>(a.scales) + s0, GROUPS);
-                } else {
-                    for (int j = 0; j < GROUPS; ++j)
-                        if (g0 + j < groups) s[j] = static_cast<const uint8_t*>(a.scales)[s0 + j];
-                }
-#pragma unroll
-                for (int j = 0; j < GROUPS; ++j) d.scale[i][j] = s[j];
-            } else {
-                uint16_t s[GROUPS] = {};
-                uint8_t z[GROUPS] = {};
-                if (!TAIL || g0 + GROUPS <= groups) {
-                    __builtin_memcpy(s, static_cast<const uint16_t*>(a.scales) + s0, 2 * GROUPS);
-                    if (a.zeros) __builtin_memcpy(z, a.zeros + row_n[i] * a.ldz + g0, GROUPS);
-                } else {
-                    for (int j = 0; j < GROUPS; ++j)
-                        if (g0 + j < groups) {
-                            s[j] = static_cast<const uint16_t*>(a.scales)[s0 + j];
-                            if (a.zeros) z[j] = a.zeros[row_n[i] * a.ldz + g0 + j];
-                        }
-                }
-#pragma unroll
-                for (int j = 0; j < GROUPS; ++j) {
-                    d.scale[i][j] = s[j];
-                    d.zero[i][j] = a.zeros ? z[j] : 8;
-                }
-            }
+            for (int j = 0; j < 4; ++j) d[i][j] = w[j];
         }
     };
     auto load_x = [&](auto tail, int64_t c, int t, Rows<XT, MB>& d) {
@@ -247,12 +256,12 @@ __global__ __launch_bounds__(64 * kWaves) void weight_matvec_kernel(MatvecArgs a
 #pragma unroll
         for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 
-    // Multiplies a chunk; MORE: and loads x of chunk `next` in the place of what
-    // has been multiplied.
-    auto multiply = [&](auto more, C& d, Rows<XT, MB>& xr, int64_t next) {
+    // Multiplies a chunk whose first group is `group` of those in LDS; MORE: and
+    // loads x of chunk `next` in the place of what has been multiplied.
+    auto multiply = [&](auto more, uint32_t (&d)[NB][4], int group, Rows<XT, MB>& xr, int64_t next) {
 #pragma unroll
         for (int j = 0; j < NB; ++j) {                          // dword (g, register) -> (register, g)
-            uint32_t(&w)[4] = d.codes[j];
+            uint32_t(&w)[4] = d[j];
             auto p = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
             auto q = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
             auto u = __builtin_amdgcn_permlane16_swap(p[0], q[0], false, false);
@@ -262,6 +271,13 @@ __global__ __launch_bounds__(64 * kWaves) void weight_matvec_kernel(MatvecArgs a
 #pragma unroll
         for (int s = 0; s < GROUPS; ++s) {
             f32x4 part[MB][NB], ones[MB];
+            float scale[NB], zero[NB];
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                const uint32_t v = lds.scales[group + s][16 * j + r];
+                scale[j] = __builtin_bit_cast(float, F == Format::FLOAT ? v : v & 0xffff0000u);
+                zero[j] = float(v & 0xffu);
+            }
 #pragma unroll
             for (int i = 0; i < MB; ++i) {
                 ones[i] = f32x4{0, 0, 0, 0};
@@ -283,8 +299,8 @@ __global__ __launch_bounds__(64 * kWaves) void weight_matvec_kernel(MatvecArgs a
                 }
 #pragma unroll
                 for (int j = 0; j < NB; ++j) {
-                    const f16 z = f16(float(d.zero[j][s]));
-                    const Frag w = unpack<HALF, F>(d.codes[j][t], f16x2{z, z});
+                    const f16 z = f16(zero[j]);
+                    const Frag w = unpack<HALF, F>(d[j][t], f16x2{z, z});
 #pragma unroll
                     for (int i = 0; i < MB; ++i) part[i][j] = product<HALF>(x[i], w, part[i][j]);
                 }
@@ -296,63 +312,77 @@ __global__ __launch_bounds__(64 * kWaves) void weight_matvec_kernel(MatvecArgs a
             }
 #pragma unroll
             for (int j = 0; j < NB; ++j) {
-                const float scale = F == Format::FLOAT ? power_of(d.scale[j][s])
-                                                       : __builtin_bit_cast(float, uint32_t(d.scale[j][s]) << 16);
-                const float z = float(d.zero[j][s]);
 #pragma unroll
                 for (int i = 0; i < MB; ++i)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float p = OFFSET ? fmadd(-z, ones[i][e], part[i][j][e]) : part[i][j][e];
-                        acc[i][j][e] = fmadd(scale, p, acc[i][j][e]);
+                        const float p = OFFSET ? fmadd(-zero[j], ones[i][e], part[i][j][e]) : part[i][j][e];
+                        acc[i][j][e] = fmadd(scale[j], p, acc[i][j][e]);
                     }
             }
         }
     };
 
-    int64_t c = wave;
-    C now;
+    constexpr int PHASE = kGroups / GROUPS;                     // chunks whose scales fit
+    uint32_t now[NB][4];
     Rows<XT, MB> xr;
-    bool any = c < whole;
-    if (any) {
-        load(std::false_type{}, c, now);
+    for (int64_t base = 0; base < chunks; base += PHASE) {
+        const int64_t end = base + PHASE < chunks ? base + PHASE : chunks;
+        const int64_t full = end < whole ? end : whole;         // of them, those that lie inside the row
+        int64_t c = base + wave;
+        bool any = c < full;
+        if (any) load(std::false_type{}, c, now);               // on its way while the scales are staged
+        const int64_t g0 = base * GROUPS, count = end * GROUPS < groups ? end * GROUPS - g0 : groups - g0;
+        if (base) __syncthreads();
+        stage(g0, int(count));
+        if (any) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t) load_x(std::false_type{}, c, t, xr);
-        for (c += waves; c < whole; c += waves) {
-            C next;
-            load(std::false_type{}, c, next);
-            multiply(std::true_type{}, now, xr, c);
-            now = next;
+            for (int t = 0; t < 4; ++t) load_x(std::false_type{}, c, t, xr);
         }
-    }
-    // the last whole chunk of this wavefront, then the partial one if its turn comes to it
-    while (any || c < chunks) {
-        if (!any) {
-            load(std::true_type{}, c, now);
+        __syncthreads();
+        if (any) {
+            for (c += waves; c < full; c += waves) {
+                uint32_t next[NB][4];
+                load(std::false_type{}, c, next);
+                multiply(std::true_type{}, now, int(c - waves - base) * GROUPS, xr, c);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) load_x(std::true_type{}, c, t, xr);
-            c = chunks;
+                for (int i = 0; i < NB; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) now[i][j] = next[i][j];
+            }
         }
-        any = false;
-        multiply(std::false_type{}, now, xr, 0);
+        // the last whole chunk of this wavefront, then the partial one if its turn comes to it
+        int64_t at = c - waves;
+        while (any || c < end) {
+            if (!any) {
+                load(std::true_type{}, c, now);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) load_x(std::true_type{}, c, t, xr);
+                at = c;
+                c = end;
+            }
+            any = false;
+            multiply(std::false_type{}, now, int(at - base) * GROUPS, xr, 0);
+        }
     }
 
+    __syncthreads();                                            // the scales' LDS is free
 #pragma unroll
     for (int i = 0; i < MB; ++i)
 #pragma unroll
         for (int j = 0; j < NB; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sums[wave][(i * NB + j) * 4 + e][lane] = acc[i][j][e];
+            for (int e = 0; e < 4; ++e) lds.sums[wave][(i * NB + j) * 4 + e][lane] = acc[i][j][e];
     __syncthreads();
 
     const int64_t rows = a.m - m0 < 16 * MB ? a.m - m0 : 16 * MB;
-    for (int e = threadIdx.x; e < int(rows) * 16 * NB; e += blockDim.x) {
-        const int ml = e / (16 * NB), nl = e % (16 * NB);       // y's row and column in the tile
+    for (int e = threadIdx.x; e < int(rows) * TILE; e += blockDim.x) {
+        const int ml = e / TILE, nl = e % TILE;       // y's row and column in the tile
         const int64_t m = m0 + ml, n = n0 + nl;
         if (n >= a.n) continue;
         const int slot = (ml / 16 * NB + nl / 16) * 4 + ml % 4, from = ml % 16 / 4 * 16 + nl % 16;
         float v = 0;
-        for (int w = 0; w < waves; ++w) v += sums[w][slot][from];
+        for (int w = 0; w < waves; ++w) v += lds.sums[w][slot][from];
         if (magnitude(v) >= kInfBits) {
             const double s = by_definition(a, XT, F, GROUP, m, n);
             v = XT == X::F8_ROW ? float(s * double(static_cast<const float*>(a.xscales)[m])) : float(s);
