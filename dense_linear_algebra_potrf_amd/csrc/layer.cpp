@@ -236,6 +236,9 @@ batchlas_status do_weight_matvec(int xtype, int xscale, int ytype, int format, i
         return fail(BATCHLAS_NOT_SUPPORTED, "m is beyond 2^21");
     if (a.n > (int64_t(1) << 24))
         return fail(BATCHLAS_NOT_SUPPORTED, "n is beyond 2^24");
+    // offsets within a tile of rows are 32-bit
+    if (a.ldx > (int64_t(1) << 27) || a.ldc > (int64_t(1) << 27))
+        return fail(BATCHLAS_NOT_SUPPORTED, "ldx or ldc is beyond 2^27");
     if (a.m == 0) return BATCHLAS_OK;
     st = bl::check_device();
     if (st != BATCHLAS_OK) return st;

@@ -105,25 +105,28 @@ __device__ __forceinline__ Frag unpack(uint32_t w, [[maybe_unused]] f16x2 zero) 
     return f;
 }
 
-// What a lane holds of x for a chunk: 8 columns of its rows for each of the
-// chunk's four products.
-template <X XT, int MB>
-struct Rows {
-    uint32_t x[MB][4][is_eight(XT) ? 2 : 4];
-    uint8_t scale[MB][4];
+// What a lane loads of a chunk: 16 bytes of a row of W per 16 rows, and of x in
+// PIECES loads per 16 rows, neighbouring lanes neighbouring columns.
+template <X XT, int MB, int NB>
+struct Held {
+    static constexpr int PIECES = is_eight(XT) ? 2 : 4;
+    u32x4 codes[NB];
+    u32x4 x[MB][PIECES];
+    uint32_t xscale[MB];          // bytes of the chunk's four blocks, of row lane % 16
 };
 
-// One element from the definition, in 64 bits.
+// One element from the definition, in 64 bits, by a whole wavefront.
 __device__ __forceinline__ double by_definition(const MatvecArgs& a, X xt, Format f, int group, int64_t m, int64_t n) {
     double sum = 0;
-    for (int64_t k = 0; k < a.k; ++k) {
+#pragma unroll 1
+    for (int64_t k = threadIdx.x & 63; k < a.k; k += 64) {
         const uint32_t u = a.codes[n * a.ldc + k / 2] >> (4 * (k & 1)) & 15;
         const int64_t g = k / group;
         double w, x;
         if (f == Format::FLOAT) {
             const uint32_t c = u & 7;
-            w = c < 2 ? 0.5 * c : ldexp(2.0 + (c & 1), int(c >> 1) - 2);
-            w = (u & 8 ? -w : w) * double(power_of(static_cast<const uint8_t*>(a.scales)[n * a.lds + g]));
+            const float v = c < 2 ? 0.5f * float(c) : __builtin_bit_cast(float, (126 + (c >> 1)) << 23 | (c & 1) << 22);
+            w = double(u & 8 ? -v : v) * double(power_of(static_cast<const uint8_t*>(a.scales)[n * a.lds + g]));
         } else {
             w = (double(u) - (a.zeros ? double(a.zeros[n * a.ldz + g]) : 8.0)) *
                 double(float(static_cast<const bf16*>(a.scales)[n * a.lds + g]));
@@ -135,6 +138,9 @@ __device__ __forceinline__ double by_definition(const MatvecArgs& a, X xt, Forma
             x *= double(power_of(static_cast<const uint8_t*>(a.xscales)[m * a.ldxs + k / kScaleBlock]));
         sum = fmadd(w, x, sum);
     }
+    if (xt == X::F8_ROW) sum *= double(static_cast<const float*>(a.xscales)[m]);
+#pragma unroll
+    for (int step = 1; step < 64; step *= 2) sum += __shfl_xor(sum, step);
     return sum;
 }
 
@@ -144,109 +150,147 @@ __global__ __launch_bounds__(64 * kWaves) void weight_matvec_kernel(MatvecArgs a
     constexpr bool OFFSET = F == Format::INTEGER && !HALF;      // zero points are taken off the sums
     constexpr int GROUPS = kChunk / GROUP, STEPS = GROUP / 32;  // groups of a chunk, products of a group
     constexpr int TILE = 16 * NB;                               // rows of W
+    constexpr int ES = EIGHT ? 1 : 2, ROW = kChunk * ES;        // bytes of an element and a chunk's row of x
+    constexpr int SPLIT = MB * ROW > 512 ? 2 : 1;               // x passes through LDS in so many parts
+    constexpr int PART = ROW / SPLIT, SLOTS = PART / 16;        // bytes and 16-byte slots of a row's part
+    constexpr int SB = F == Format::FLOAT ? 1 : 2;              // bytes of a scale
+    using H = Held<XT, MB, NB>;
+    __shared__ uint32_t scales[kGroups][TILE];                  // of the groups at hand
     __shared__ union {
-        uint32_t scales[kGroups][TILE];                         // of the groups at hand, as `scale_of` reads them
+        struct { u32x4 codes[NB * 64]; u32x4 x[16 * MB * SLOTS]; } of[kWaves];
         float sums[kWaves][MB * NB * 4][64];
     } lds;
 
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
-    const int r = lane & 15, g = lane >> 4;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int waves = blockDim.x >> 6, r = lane & 15, g = lane >> 4;
     const int64_t n0 = int64_t(blockIdx.x) * TILE, m0 = int64_t(blockIdx.y) * (16 * MB);
     const int64_t chunks = (a.k + kChunk - 1) / kChunk, whole = a.k / kChunk;
     const int64_t groups = (a.k + GROUP - 1) / GROUP;
-
-    // rows past the end read the last one; their results are not stored
-    int64_t row_n[NB], row_m[MB];
-#pragma unroll
-    for (int i = 0; i < NB; ++i) row_n[i] = n0 + 16 * i + r < a.n ? n0 + 16 * i + r : a.n - 1;
-#pragma unroll
-    for (int i = 0; i < MB; ++i) row_m[i] = m0 + 16 * i + r < a.m ? m0 + 16 * i + r : a.m - 1;
+    const int rows_n = a.n - n0 < TILE ? int(a.n - n0) : TILE, rows_m = a.m - m0 < 16 * MB ? int(a.m - m0) : 16 * MB;
 
     // Scales of the groups from `first` on, to LDS: a float's upper half and, for
     // integers, the zero point in the lower.  Neighbouring lanes take neighbouring
     // rows and 8 groups each, so that the writes spread over the banks.  Groups
     // that the last chunk lacks get a finite scale; their products are zero.
     auto stage = [&](int64_t first, int count) {
-        const int rounded = (count + GROUPS - 1) / GROUPS * GROUPS, octets = (rounded + 7) / 8;
-        for (int e = threadIdx.x; e < octets * TILE; e += blockDim.x) {
+        const int rounded = (count + GROUPS - 1) / GROUPS * GROUPS;
+        for (int e = threadIdx.x; e < (rounded + 7) / 8 * TILE; e += blockDim.x) {
             const int row = e % TILE, at = e / TILE * 8, left = count - at;
-            const int64_t n = n0 + row < a.n ? n0 + row : a.n - 1, s0 = n * a.lds + first + at;
-            uint32_t v[8];
-            if constexpr (F == Format::FLOAT) {
-                const uint8_t* p = static_cast<const uint8_t*>(a.scales) + s0;
-                uint8_t s[8] = {};
-                if (left >= 8) __builtin_memcpy(s, p, 8);
-                else
-                    for (int j = 0; j < 7; ++j) s[j] = j < left ? p[j] : 0;
+            const int64_t n = n0 + row < a.n ? n0 + row : a.n - 1;
+            const uint8_t* p = static_cast<const uint8_t*>(a.scales) + (n * a.lds + first + at) * SB;
+            const uint8_t* q = a.zeros + n * a.ldz + first + at;
+            if (left >= 8) {
+                uint8_t s[8 * SB], z[8] = {8, 8, 8, 8, 8, 8, 8, 8};
+                __builtin_memcpy(s, p, sizeof(s));
+                if (SB == 2 && a.zeros) __builtin_memcpy(z, q, 8);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = __builtin_bit_cast(uint32_t, power_of(s[j]));
+                for (int j = 0; j < 8; ++j)
+                    scales[at + j][row] = SB == 1 ? __builtin_bit_cast(uint32_t, power_of(s[j]))
+                                                  : uint32_t(s[j * SB + SB - 1]) << 24 | uint32_t(s[j * SB]) << 16 | z[j];
             } else {
-                const uint16_t* p = static_cast<const uint16_t*>(a.scales) + s0;
-                const uint8_t* q = a.zeros + n * a.ldz + first + at;
-                uint16_t s[8] = {};
-                uint8_t z[8] = {8, 8, 8, 8, 8, 8, 8, 8};
-                if (left >= 8) {
-                    __builtin_memcpy(s, p, 16);
-                    if (a.zeros) __builtin_memcpy(z, q, 8);
-                } else {
-                    for (int j = 0; j < 7; ++j) {
-                        s[j] = j < left ? p[j] : 0;
-                        if (a.zeros) z[j] = j < left ? q[j] : 0;
-                    }
+#pragma unroll 1
+                for (int j = 0; j < 8 && at + j < rounded; ++j) {
+                    uint32_t v = 0;
+                    if (j < left)
+                        v = SB == 1 ? __builtin_bit_cast(uint32_t, power_of(p[j]))
+                                    : uint32_t(p[j * SB + SB - 1]) << 24 | uint32_t(p[j * SB]) << 16 | (a.zeros ? q[j] : 8);
+                    scales[at + j][row] = v;
                 }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = uint32_t(s[j]) << 16 | z[j];
             }
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (at + j < rounded) lds.scales[at + j][row] = v[j];
         }
     };
 
-    // TAIL: the last chunk, which ends inside; what is past the row's end is zero.
-    auto load = [&](auto tail, int64_t c, uint32_t (&d)[NB][4]) {
+    // Loads a chunk that lies inside the row.  Codes: lane / 4 is the row, lane % 4
+    // the 16 bytes of it.  x: 64 / PER rows a load, PER lanes a row.  Rows past the
+    // end are not read: their results are not stored.
+    constexpr int PER = ROW / 16, STEP = 64 / PER;
+    const uint32_t code_at = uint32_t(lane >> 2) * uint32_t(a.ldc) + 16 * (lane & 3);
+    const uint32_t x_at = uint32_t(lane / PER) * uint32_t(a.ldx * ES) + 16 * (lane % PER);
+    auto load = [&](int64_t c, H& d) {
+        const uint8_t* codes = a.codes + n0 * a.ldc + c * (kChunk / 2);
 #pragma unroll
-        for (int i = 0; i < NB; ++i) {
-            const int64_t at = c * (kChunk / 2) + 16 * g;
-            u32x4 w = {0, 0, 0, 0};
-            if (!decltype(tail)::value || at < (a.k + 1) / 2)
-                w = *reinterpret_cast<const u32x4*>(a.codes + row_n[i] * a.ldc + at);
+        for (int i = 0; i < NB; ++i, codes += 16 * a.ldc)
+            if (16 * i + (lane >> 2) < rows_n) d.codes[i] = *reinterpret_cast<const u32x4*>(codes + code_at);
+        const uint8_t* x = static_cast<const uint8_t*>(a.x) + (m0 * a.ldx + c * kChunk) * ES;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) d[i][j] = w[j];
+        for (int i = 0; i < MB; ++i)
+#pragma unroll
+            for (int q = 0; q < H::PIECES; ++q, x += STEP * a.ldx * ES)
+                if (16 * i + STEP * q + lane / PER < rows_m) __builtin_memcpy(&d.x[i][q], x + x_at, 16);
+        if constexpr (XT == X::F8_BLOCK) {
+#pragma unroll
+            for (int i = 0; i < MB; ++i)
+                if (16 * i + r < rows_m)
+                    __builtin_memcpy(&d.xscale[i], static_cast<const uint8_t*>(a.xscales) + (m0 + 16 * i + r) * a.ldxs + c * 4, 4);
         }
     };
-    auto load_x = [&](auto tail, int64_t c, int t, Rows<XT, MB>& d) {
-        constexpr bool TAIL = decltype(tail)::value;
-        const int64_t k = c * kChunk + 32 * t + 8 * g;
+
+    // Into this wavefront's LDS.  The 16-byte slots of a row are permuted by the
+    // row, so that the reads below (16 rows at a time) spread over all banks.
+    auto& own = lds.of[wave];
+    auto put_codes = [&](const H& d) {
 #pragma unroll
-        for (int i = 0; i < MB; ++i) {
-            if constexpr (EIGHT) {
-                const uint8_t* p = static_cast<const uint8_t*>(a.x) + row_m[i] * a.ldx + k;
-                uint64_t v = 0;
-                if (!TAIL || k + 8 <= a.k) {
-                    __builtin_memcpy(&v, p, 8);
-                } else {
-                    for (int j = 0; j < 8; ++j)
-                        if (k + j < a.k) v |= uint64_t(p[j]) << (8 * j);
-                }
-                d.x[i][t][0] = uint32_t(v);
-                d.x[i][t][1] = uint32_t(v >> 32);
-                if constexpr (XT == X::F8_BLOCK) {
-                    const int64_t b = c * 4 + t;
-                    d.scale[i][t] = !TAIL || b * kScaleBlock < a.k
-                                        ? static_cast<const uint8_t*>(a.xscales)[row_m[i] * a.ldxs + b] : 127;
-                }
-            } else {
-                const uint16_t* p = static_cast<const uint16_t*>(a.x) + row_m[i] * a.ldx + k;
-                if (!TAIL || k + 8 <= a.k) {
-                    __builtin_memcpy(d.x[i][t], p, 16);
-                } else {
-                    uint16_t v[8] = {};
-                    for (int j = 0; j < 8; ++j)
-                        if (k + j < a.k) v[j] = p[j];
-                    __builtin_memcpy(d.x[i][t], v, 16);
-                }
+        for (int i = 0; i < NB; ++i) own.codes[64 * i + (lane & ~3) + ((lane & 3) ^ (lane >> 4))] = d.codes[i];
+    };
+    // Permutation of the slots of row q of a part.
+    auto mix = [](int q) { return SLOTS >= 16 ? q & 15 : SLOTS == 8 ? q >> 1 & 7 : q >> 2 & 3; };
+    auto put_x = [&](const H& d, int part) {
+#pragma unroll
+        for (int i = 0; i < MB; ++i)
+#pragma unroll
+            for (int q = 0; q < H::PIECES; ++q) {
+                const int row = STEP * q + lane / PER, slot = lane % PER - part * SLOTS;
+                if (SPLIT == 1 || (slot >= 0 && slot < SLOTS)) own.x[(16 * i + row) * SLOTS + (slot ^ mix(row))] = d.x[i][q];
             }
+    };
+    // The last chunk, which ends inside, straight to LDS (the scales of its blocks
+    // to `d`): what is past the row's end is zero.
+    const int left = int(a.k - whole * kChunk);                 // columns of it
+    auto put_partial = [&](H& d, int part) {
+        const uint8_t* codes = a.codes + n0 * a.ldc + whole * (kChunk / 2);
+        if (part == 0)
+#pragma unroll 1
+            for (int i = 0; i < NB; ++i) {
+                u32x4 v = {0, 0, 0, 0};
+                if (16 * i + (lane >> 2) < rows_n && 16 * (lane & 3) < (left + 1) / 2)
+                    v = *reinterpret_cast<const u32x4*>(codes + 16 * i * a.ldc + code_at);
+                own.codes[64 * i + (lane & ~3) + ((lane & 3) ^ (lane >> 4))] = v;
+            }
+        const uint8_t* x = static_cast<const uint8_t*>(a.x) + (m0 * a.ldx + whole * kChunk) * ES;
+#pragma unroll 1
+        for (int e = lane; e < 16 * MB * (PART / ES); e += 64) {
+            const int row = e / (PART / ES), byte = e % (PART / ES) * ES, k = part * (PART / ES) + e % (PART / ES);
+            uint8_t* to = reinterpret_cast<uint8_t*>(&own.x[row * SLOTS + (byte / 16 ^ mix(row))]) + byte % 16;
+            const bool in = row < rows_m && k < left;
+            if constexpr (EIGHT) *to = in ? x[row * a.ldx + k] : 0;
+            else *reinterpret_cast<uint16_t*>(to) = in ? reinterpret_cast<const uint16_t*>(x)[row * a.ldx + k] : 0;
+        }
+        if constexpr (XT == X::F8_BLOCK) {
+#pragma unroll
+            for (int i = 0; i < MB; ++i) {
+                uint32_t v = 0x7f7f7f7fu;
+                if (part == 0 && 16 * i + r < rows_m) {
+                    const uint8_t* p = static_cast<const uint8_t*>(a.xscales) + (m0 + 16 * i + r) * a.ldxs + whole * 4;
+#pragma unroll 1
+                    for (int j = 0; j * kScaleBlock < left; ++j) v = (v & ~(255u << (8 * j))) | uint32_t(p[j]) << (8 * j);
+                }
+                if (part == 0) d.xscale[i] = v;
+            }
+        }
+    };
+    // Codes of product t for row lane % 16 of W: dword 4 t + lane / 16 of the row.
+    auto get_codes = [&](int i, int t) {
+        return reinterpret_cast<const uint32_t*>(&own.codes[64 * i + 4 * r + (t ^ (r >> 2))])[g];
+    };
+    // Columns 32 t + 8 g of row lane % 16 of x.
+    auto get_x = [&](int i, int t, [[maybe_unused]] uint32_t scale) {
+        const int byte = (32 * t + 8 * g) * ES % PART;
+        const uint32_t* p = reinterpret_cast<const uint32_t*>(&own.x[(16 * i + r) * SLOTS + (byte / 16 ^ mix(r))]);
+        if constexpr (EIGHT) {
+            const uint2 v = reinterpret_cast<const uint2*>(p)[g & 1];
+            return from_e4m3<HALF>(v.x, v.y, XT == X::F8_BLOCK ? power_of(scale >> (8 * t) & 255u) : 1.0f);
+        } else {
+            return *reinterpret_cast<const Frag*>(p);
         }
     };
 
@@ -256,25 +300,28 @@ __global__ __launch_bounds__(64 * kWaves) void weight_matvec_kernel(MatvecArgs a
 #pragma unroll
         for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 
-    // Multiplies a chunk whose first group is `group` of those in LDS; MORE: and
-    // loads x of chunk `next` in the place of what has been multiplied.
-    auto multiply = [&](auto more, uint32_t (&d)[NB][4], int group, Rows<XT, MB>& xr, int64_t next) {
-#pragma unroll
-        for (int j = 0; j < NB; ++j) {                          // dword (g, register) -> (register, g)
-            uint32_t(&w)[4] = d[j];
-            auto p = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
-            auto q = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
-            auto u = __builtin_amdgcn_permlane16_swap(p[0], q[0], false, false);
-            auto v = __builtin_amdgcn_permlane16_swap(p[1], q[1], false, false);
-            w[0] = u[0], w[1] = u[1], w[2] = v[0], w[3] = v[1];
+    // Multiplies chunk c, which is held if it lies inside the row, and loads chunk
+    // `next` if that does; `group`: its first group, of those staged.
+    auto multiply = [&](H& d, int64_t c, int group, int64_t next) {
+        wave_lds_sync();                                        // the last chunk has been read
+        if (c < whole) {
+            put_codes(d);
+            put_x(d, 0);
+        } else {
+            put_partial(d, 0);
         }
+        uint32_t xscale[MB];
+#pragma unroll
+        for (int i = 0; i < MB; ++i) xscale[i] = XT == X::F8_BLOCK ? d.xscale[i] : 0;
+        if (SPLIT == 1 && next < whole) load(next, d);
+        wave_lds_sync();
 #pragma unroll
         for (int s = 0; s < GROUPS; ++s) {
             f32x4 part[MB][NB], ones[MB];
             float scale[NB], zero[NB];
 #pragma unroll
             for (int j = 0; j < NB; ++j) {
-                const uint32_t v = lds.scales[group + s][16 * j + r];
+                const uint32_t v = scales[group + s][16 * j + r];
                 scale[j] = __builtin_bit_cast(float, F == Format::FLOAT ? v : v & 0xffff0000u);
                 zero[j] = float(v & 0xffu);
             }
@@ -287,27 +334,26 @@ __global__ __launch_bounds__(64 * kWaves) void weight_matvec_kernel(MatvecArgs a
 #pragma unroll
             for (int q = 0; q < STEPS; ++q) {
                 const int t = s * STEPS + q;
+                if (SPLIT == 2 && t == 2) {
+                    wave_lds_sync();
+                    if (c < whole) put_x(d, 1);
+                    else put_partial(d, 1);
+                    if (next < whole) load(next, d);
+                    wave_lds_sync();
+                }
                 Frag x[MB];
 #pragma unroll
                 for (int i = 0; i < MB; ++i) {
-                    if constexpr (EIGHT)
-                        x[i] = from_e4m3<HALF>(xr.x[i][t][0], xr.x[i][t][1], XT == X::F8_BLOCK ? power_of(xr.scale[i][t]) : 1.0f);
-                    else
-                        x[i] = Frag{{xr.x[i][t][0], xr.x[i][t][1], xr.x[i][t][2], xr.x[i][t][3]}};
+                    x[i] = get_x(i, t, xscale[i]);
                     if constexpr (OFFSET)
                         ones[i] = product<HALF>(x[i], Frag{{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u}}, ones[i]);
                 }
 #pragma unroll
                 for (int j = 0; j < NB; ++j) {
                     const f16 z = f16(zero[j]);
-                    const Frag w = unpack<HALF, F>(d[j][t], f16x2{z, z});
+                    const Frag w = unpack<HALF, F>(get_codes(j, t), f16x2{z, z});
 #pragma unroll
                     for (int i = 0; i < MB; ++i) part[i][j] = product<HALF>(x[i], w, part[i][j]);
-                }
-                if constexpr (decltype(more)::value) {
-                    // not earlier: x would be held twice
-                    __builtin_amdgcn_sched_barrier(0);
-                    load_x(std::false_type{}, next, t, xr);
                 }
             }
 #pragma unroll
@@ -324,49 +370,19 @@ __global__ __launch_bounds__(64 * kWaves) void weight_matvec_kernel(MatvecArgs a
     };
 
     constexpr int PHASE = kGroups / GROUPS;                     // chunks whose scales fit
-    uint32_t now[NB][4];
-    Rows<XT, MB> xr;
+    H held = {};
     for (int64_t base = 0; base < chunks; base += PHASE) {
         const int64_t end = base + PHASE < chunks ? base + PHASE : chunks;
-        const int64_t full = end < whole ? end : whole;         // of them, those that lie inside the row
         int64_t c = base + wave;
-        bool any = c < full;
-        if (any) load(std::false_type{}, c, now);               // on its way while the scales are staged
-        const int64_t g0 = base * GROUPS, count = end * GROUPS < groups ? end * GROUPS - g0 : groups - g0;
+        if (c < end && c < whole) load(c, held);                // on its way while the scales are staged
+        const int64_t g0 = base * GROUPS;
         if (base) __syncthreads();
-        stage(g0, int(count));
-        if (any) {
-#pragma unroll
-            for (int t = 0; t < 4; ++t) load_x(std::false_type{}, c, t, xr);
-        }
+        stage(g0, int(end * GROUPS < groups ? end * GROUPS - g0 : groups - g0));
         __syncthreads();
-        if (any) {
-            for (c += waves; c < full; c += waves) {
-                uint32_t next[NB][4];
-                load(std::false_type{}, c, next);
-                multiply(std::true_type{}, now, int(c - waves - base) * GROUPS, xr, c);
-#pragma unroll
-                for (int i = 0; i < NB; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) now[i][j] = next[i][j];
-            }
-        }
-        // the last whole chunk of this wavefront, then the partial one if its turn comes to it
-        int64_t at = c - waves;
-        while (any || c < end) {
-            if (!any) {
-                load(std::true_type{}, c, now);
-#pragma unroll
-                for (int t = 0; t < 4; ++t) load_x(std::true_type{}, c, t, xr);
-                at = c;
-                c = end;
-            }
-            any = false;
-            multiply(std::false_type{}, now, int(at - base) * GROUPS, xr, 0);
-        }
+        for (; c < end; c += waves) multiply(held, c, int(c - base) * GROUPS, c + waves < end ? c + waves : whole);
     }
 
-    __syncthreads();                                            // the scales' LDS is free
+    __syncthreads();                                            // the chunks' LDS is free
 #pragma unroll
     for (int i = 0; i < MB; ++i)
 #pragma unroll
@@ -375,24 +391,27 @@ __global__ __launch_bounds__(64 * kWaves) void weight_matvec_kernel(MatvecArgs a
             for (int e = 0; e < 4; ++e) lds.sums[wave][(i * NB + j) * 4 + e][lane] = acc[i][j][e];
     __syncthreads();
 
-    const int64_t rows = a.m - m0 < 16 * MB ? a.m - m0 : 16 * MB;
-    for (int e = threadIdx.x; e < int(rows) * TILE; e += blockDim.x) {
-        const int ml = e / TILE, nl = e % TILE;       // y's row and column in the tile
+    // whole wavefronts: the detour below takes all lanes
+    for (int e0 = threadIdx.x & ~63; e0 < rows_m * TILE; e0 += blockDim.x) {
+        const int e = e0 + lane, ml = e / TILE, nl = e % TILE;  // y's row and column in the tile
         const int64_t m = m0 + ml, n = n0 + nl;
-        if (n >= a.n) continue;
+        const bool in = ml < rows_m && nl < rows_n;
         const int slot = (ml / 16 * NB + nl / 16) * 4 + ml % 4, from = ml % 16 / 4 * 16 + nl % 16;
         float v = 0;
-        for (int w = 0; w < waves; ++w) v += lds.sums[w][slot][from];
-        if (magnitude(v) >= kInfBits) {
-            const double s = by_definition(a, XT, F, GROUP, m, n);
-            v = XT == X::F8_ROW ? float(s * double(static_cast<const float*>(a.xscales)[m])) : float(s);
-        } else if (XT == X::F8_ROW) {
-            v *= static_cast<const float*>(a.xscales)[m];
+        if (in) {
+            for (int w = 0; w < waves; ++w) v += lds.sums[w][slot][from];
+            if (XT == X::F8_ROW) v *= static_cast<const float*>(a.xscales)[m];
         }
-        const int64_t at = m * a.ldy + n;
-        if (yt == Type::F32) static_cast<float*>(a.y)[at] = v;
-        else if (yt == Type::F16) static_cast<f16*>(a.y)[at] = f16(v);
-        else static_cast<bf16*>(a.y)[at] = bf16(v);
+        for (uint64_t odd = __ballot(magnitude(v) >= kInfBits); odd; odd &= odd - 1) {
+            const int at = __builtin_ctzll(odd);
+            const double d = by_definition(a, XT, F, GROUP, m0 + (e0 + at) / TILE, n0 + (e0 + at) % TILE);
+            if (lane == at) v = float(d);
+        }
+        if (!in) continue;
+        const int64_t to = m * a.ldy + n;
+        if (yt == Type::F32) static_cast<float*>(a.y)[to] = v;
+        else if (yt == Type::F16) static_cast<f16*>(a.y)[to] = f16(v);
+        else static_cast<bf16*>(a.y)[to] = bf16(v);
     }
 }
 
