@@ -13,11 +13,10 @@
 // its natural order.
 //
 // Integer codes become 16-bit floats through the 8-bit conversion: the byte
-// 0000uuuu read as e4m3 is u 2^-9 for every u in 0..15, subnormal or not.  For
-// half-precision x the zero point is subtracted there (exact); bfloat16 has no
-// packed subtraction, so the product takes u as it is and z times the sum of x
-// over the group, from a product with ones, is taken off afterwards.  Scales are
-// applied to the sums in 32 bits.
+// 0000uuuu read as e4m3 is u 2^-9 for every u in 0..15, subnormal or not.  The
+// product takes u as it is, and z times the sum of x over the group, from a
+// product with ones, is taken off afterwards.  Scales are applied to the sums in
+// 32 bits.
 //
 // The detours (codes without their scale, codes without their zero point) give
 // the definition's result wherever they are finite.  Where they are not, the
@@ -33,8 +32,6 @@ using namespace layer;
 
 using bf16x8 = bf16 __attribute__((ext_vector_type(8)));
 using f16x8 = f16 __attribute__((ext_vector_type(8)));
-using bf16x2 = bf16 __attribute__((ext_vector_type(2)));
-using f16x2 = f16 __attribute__((ext_vector_type(2)));
 using f32x4 = float __attribute__((ext_vector_type(4)));
 using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
 
@@ -45,7 +42,6 @@ constexpr bool in_half(X x) { return x == X::F16 || x == X::F8_ROW; }
 constexpr bool is_eight(X x) { return x == X::F8_BLOCK || x == X::F8_ROW; }
 
 constexpr int kChunk = 128;       // columns a wavefront takes at a time
-constexpr int kWaves = 8;         // wavefronts of a workgroup, at most
 constexpr int kGroups = 256;      // groups of a row whose scales are in LDS at a time
 
 // Eight columns of a row as the matrix cores take them: words of two 16-bit floats.
@@ -76,10 +72,10 @@ __device__ __forceinline__ Frag from_e4m3(uint32_t lo, uint32_t hi, float scale)
     return f;
 }
 
-// Codes of 8 columns (a dword) as floats; integers less `zero` (packed halves)
-// for half precision, and as they are for bfloat16.
-template <bool HALF, Format F>
-__device__ __forceinline__ Frag unpack(uint32_t w, [[maybe_unused]] f16x2 zero) {
+// Codes of 8 columns (a dword) as floats, integers as they are (0..15) and in
+// the order of their half bytes (MIXED: 0 2 4 6 1 3 5 7) or in that of the columns.
+template <bool HALF, Format F, bool MIXED>
+__device__ __forceinline__ Frag unpack(uint32_t w) {
     Frag f;
     if constexpr (F == Format::FLOAT) {
         if constexpr (HALF) {
@@ -95,24 +91,53 @@ __device__ __forceinline__ Frag unpack(uint32_t w, [[maybe_unused]] f16x2 zero) 
         }
     } else {
         const uint32_t even = w & 0x0f0f0f0fu, odd = w >> 4 & 0x0f0f0f0fu;
-        f = from_e4m3<HALF>(__builtin_amdgcn_perm(odd, even, 0x05010400u),
-                            __builtin_amdgcn_perm(odd, even, 0x07030602u), 512.0f);
-        if constexpr (HALF) {
-#pragma unroll
-            for (uint32_t& v : f.word) v = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, v) - zero);
-        }
+        if constexpr (MIXED) f = from_e4m3<HALF>(even, odd, 512.0f);
+        else f = from_e4m3<HALF>(__builtin_amdgcn_perm(odd, even, 0x05010400u), __builtin_amdgcn_perm(odd, even, 0x07030602u), 512.0f);
     }
     return f;
 }
 
+// Columns 0..7 in the order 0 2 4 6 1 3 5 7, for each 8 of a piece.
+template <bool EIGHT>
+__device__ __forceinline__ u32x4 mixed(u32x4 v) {
+    constexpr uint32_t LO = EIGHT ? 0x06040200u : 0x05040100u, HI = EIGHT ? 0x07050301u : 0x07060302u;
+    auto perm = [](uint32_t a, uint32_t b, uint32_t s) { return uint32_t(__builtin_amdgcn_perm(a, b, s)); };
+    if constexpr (EIGHT) return u32x4{perm(v[1], v[0], LO), perm(v[1], v[0], HI), perm(v[3], v[2], LO), perm(v[3], v[2], HI)};
+    else return u32x4{perm(v[1], v[0], LO), perm(v[3], v[2], LO), perm(v[1], v[0], HI), perm(v[3], v[2], HI)};
+}
+
+// The first `bytes` (of elements of ES bytes) of 16 at p, the others zero.  Where
+// the row holds 16 bytes at least (is_long), one load of the 16 that end with them.
+template <int ES>
+__device__ __forceinline__ u32x4 load_start(const uint8_t* p, int bytes, bool is_long) {
+    using u64x2 = uint64_t __attribute__((ext_vector_type(2)));
+    u64x2 v = {0, 0};
+    if (bytes >= 16) {
+        __builtin_memcpy(&v, p, 16);
+    } else if (is_long) {
+        __builtin_memcpy(&v, p + bytes - 16, 16);
+        const int cut = 8 * (16 - bytes);                       // 8..120 bits
+        v = cut < 64 ? u64x2{v[0] >> cut | v[1] << (64 - cut), v[1] >> cut} : u64x2{v[1] >> (cut - 64), 0};
+    } else {
+#pragma unroll 1
+        for (int j = 0; j < bytes; j += ES) {
+            uint64_t e = p[j];
+            if constexpr (ES == 2) e |= uint64_t(p[j + 1]) << 8;
+            if (j < 8) v[0] |= e << (8 * j);
+            else v[1] |= e << (8 * j - 64);
+        }
+    }
+    return __builtin_bit_cast(u32x4, v);
+}
+
 // What a lane loads of a chunk: 16 bytes of a row of W per 16 rows, and of x in
-// PIECES loads per 16 rows, neighbouring lanes neighbouring columns.
-template <X XT, int MB, int NB>
+// PIECES loads, neighbouring lanes neighbouring columns.
+template <X XT, int MT, int NB>
 struct Held {
-    static constexpr int PIECES = is_eight(XT) ? 2 : 4;
+    static constexpr int BYTES = MT * kChunk * (is_eight(XT) ? 1 : 2), PIECES = (BYTES + 1023) / 1024;
     u32x4 codes[NB];
-    u32x4 x[MB][PIECES];
-    uint32_t xscale[MB];          // bytes of the chunk's four blocks, of row lane % 16
+    u32x4 x[PIECES];
+    uint32_t xscale[(MT + 15) / 16];   // bytes of the chunk's four blocks, of row lane % 16
 };
 
 // One element from the definition, in 64 bits, by a whole wavefront.
@@ -144,35 +169,39 @@ __device__ __forceinline__ double by_definition(const MatvecArgs& a, X xt, Forma
     return sum;
 }
 
-template <X XT, Format F, int GROUP, int MB, int NB>
-__global__ __launch_bounds__(64 * kWaves) void weight_matvec_kernel(MatvecArgs a, Type yt) {
+template <X XT, Format F, int GROUP, int MT, int NB, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void weight_matvec_kernel(MatvecArgs a, Type yt) {
     constexpr bool HALF = in_half(XT), EIGHT = is_eight(XT);
-    constexpr bool OFFSET = F == Format::INTEGER && !HALF;      // zero points are taken off the sums
+    constexpr int MB = (MT + 15) / 16;                          // tiles of 16 rows of x, the last partly empty
+    constexpr bool OFFSET = F == Format::INTEGER;               // zero points are taken off the sums
     constexpr int GROUPS = kChunk / GROUP, STEPS = GROUP / 32;  // groups of a chunk, products of a group
     constexpr int TILE = 16 * NB;                               // rows of W
     constexpr int ES = EIGHT ? 1 : 2, ROW = kChunk * ES;        // bytes of an element and a chunk's row of x
-    constexpr int SPLIT = MB * ROW > 512 ? 2 : 1;               // x passes through LDS in so many parts
-    constexpr int PART = ROW / SPLIT, SLOTS = PART / 16;        // bytes and 16-byte slots of a row's part
+    constexpr int SLOTS = ROW / 16;                             // of 16 bytes
     constexpr int SB = F == Format::FLOAT ? 1 : 2;              // bytes of a scale
-    using H = Held<XT, MB, NB>;
+    using H = Held<XT, MT, NB>;
+    // integers come apart in a mixed order: x is mixed alike on its way into LDS,
+    // or the codes on their way out of it, whichever is less
+    constexpr bool MIXED = F == Format::INTEGER && 4 * H::PIECES <= 8 * NB;
+    constexpr int SUMS = MT < 4 ? MT : 4;                       // of a lane's four sums, those of rows of x
     __shared__ uint32_t scales[kGroups][TILE];                  // of the groups at hand
     __shared__ union {
-        struct { u32x4 codes[NB * 64]; u32x4 x[16 * MB * SLOTS]; } of[kWaves];
-        float sums[kWaves][MB * NB * 4][64];
+        struct { u32x4 codes[NB * 64]; u32x4 x[MT * SLOTS]; } of[WAVES];
+        float sums[WAVES][MB * NB * 4][64];
     } lds;
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int waves = blockDim.x >> 6, r = lane & 15, g = lane >> 4;
-    const int64_t n0 = int64_t(blockIdx.x) * TILE, m0 = int64_t(blockIdx.y) * (16 * MB);
-    const int64_t chunks = (a.k + kChunk - 1) / kChunk, whole = a.k / kChunk;
-    const int64_t groups = (a.k + GROUP - 1) / GROUP;
-    const int rows_n = a.n - n0 < TILE ? int(a.n - n0) : TILE, rows_m = a.m - m0 < 16 * MB ? int(a.m - m0) : 16 * MB;
+    const int64_t n0 = int64_t(blockIdx.x) * TILE, m0 = int64_t(blockIdx.y) * MT;
+    const int chunks = int((a.k + kChunk - 1) / kChunk), whole = int(a.k / kChunk);
+    const int groups = int((a.k + GROUP - 1) / GROUP);
+    const int rows_n = a.n - n0 < TILE ? int(a.n - n0) : TILE, rows_m = a.m - m0 < MT ? int(a.m - m0) : MT;
 
     // Scales of the groups from `first` on, to LDS: a float's upper half and, for
     // integers, the zero point in the lower.  Neighbouring lanes take neighbouring
     // rows and 8 groups each, so that the writes spread over the banks.  Groups
     // that the last chunk lacks get a finite scale; their products are zero.
-    auto stage = [&](int64_t first, int count) {
+    auto stage = [&](int first, int count) {
         const int rounded = (count + GROUPS - 1) / GROUPS * GROUPS;
         for (int e = threadIdx.x; e < (rounded + 7) / 8 * TILE; e += blockDim.x) {
             const int row = e % TILE, at = e / TILE * 8, left = count - at;
@@ -206,22 +235,53 @@ __global__ __launch_bounds__(64 * kWaves) void weight_matvec_kernel(MatvecArgs a
     constexpr int PER = ROW / 16, STEP = 64 / PER;
     const uint32_t code_at = uint32_t(lane >> 2) * uint32_t(a.ldc) + 16 * (lane & 3);
     const uint32_t x_at = uint32_t(lane / PER) * uint32_t(a.ldx * ES) + 16 * (lane % PER);
-    auto load = [&](int64_t c, H& d) {
-        const uint8_t* codes = a.codes + n0 * a.ldc + c * (kChunk / 2);
+    const uint8_t* const codes0 = a.codes + n0 * a.ldc;
+    const uint8_t* const x0 = static_cast<const uint8_t*>(a.x) + m0 * a.ldx * ES;
+    const int64_t codes_step = 16 * a.ldc, x_step = STEP * a.ldx * ES;
+    auto load = [&](int c, H& d) {
+        const uint8_t* codes = codes0 + int64_t(c) * (kChunk / 2);
 #pragma unroll
-        for (int i = 0; i < NB; ++i, codes += 16 * a.ldc)
+        for (int i = 0; i < NB; ++i, codes += codes_step)
             if (16 * i + (lane >> 2) < rows_n) d.codes[i] = *reinterpret_cast<const u32x4*>(codes + code_at);
-        const uint8_t* x = static_cast<const uint8_t*>(a.x) + (m0 * a.ldx + c * kChunk) * ES;
+        const uint8_t* x = x0 + int64_t(c) * ROW;
 #pragma unroll
-        for (int i = 0; i < MB; ++i)
-#pragma unroll
-            for (int q = 0; q < H::PIECES; ++q, x += STEP * a.ldx * ES)
-                if (16 * i + STEP * q + lane / PER < rows_m) __builtin_memcpy(&d.x[i][q], x + x_at, 16);
+        for (int q = 0; q < H::PIECES; ++q, x += x_step)
+            if (STEP * q + lane / PER < rows_m) __builtin_memcpy(&d.x[q], x + x_at, 16);
         if constexpr (XT == X::F8_BLOCK) {
 #pragma unroll
             for (int i = 0; i < MB; ++i)
                 if (16 * i + r < rows_m)
                     __builtin_memcpy(&d.xscale[i], static_cast<const uint8_t*>(a.xscales) + (m0 + 16 * i + r) * a.ldxs + c * 4, 4);
+        }
+    };
+
+    // Loads the last chunk, which ends inside: what is past the row's end is zero.
+    const int left = int(a.k - int64_t(whole) * kChunk);        // columns of it
+    auto load_partial = [&](H& d) {
+        const uint8_t* codes = codes0 + int64_t(whole) * (kChunk / 2);
+#pragma unroll
+        for (int i = 0; i < NB; ++i, codes += codes_step) {
+            d.codes[i] = u32x4{0, 0, 0, 0};
+            if (16 * i + (lane >> 2) < rows_n && 16 * (lane & 3) < (left + 1) / 2)
+                d.codes[i] = *reinterpret_cast<const u32x4*>(codes + code_at);
+        }
+        const uint8_t* x = x0 + int64_t(whole) * ROW;
+        const int bytes = left * ES - 16 * (lane % PER);        // of this lane's piece
+#pragma unroll
+        for (int q = 0; q < H::PIECES; ++q, x += x_step) {
+            d.x[q] = u32x4{0, 0, 0, 0};
+            if (STEP * q + lane / PER < rows_m && bytes > 0) d.x[q] = load_start<ES>(x + x_at, bytes, a.k * ES >= 16);
+        }
+        if constexpr (XT == X::F8_BLOCK) {
+#pragma unroll
+            for (int i = 0; i < MB; ++i) {
+                d.xscale[i] = 0x7f7f7f7fu;
+                if (16 * i + r >= rows_m) continue;
+                const uint8_t* p = static_cast<const uint8_t*>(a.xscales) + (m0 + 16 * i + r) * a.ldxs + whole * 4;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (j * kScaleBlock < left) d.xscale[i] = (d.xscale[i] & ~(255u << (8 * j))) | uint32_t(p[j]) << (8 * j);
+            }
         }
     };
 
@@ -232,50 +292,12 @@ __global__ __launch_bounds__(64 * kWaves) void weight_matvec_kernel(MatvecArgs a
 #pragma unroll
         for (int i = 0; i < NB; ++i) own.codes[64 * i + (lane & ~3) + ((lane & 3) ^ (lane >> 4))] = d.codes[i];
     };
-    // Permutation of the slots of row q of a part.
-    auto mix = [](int q) { return SLOTS >= 16 ? q & 15 : SLOTS == 8 ? q >> 1 & 7 : q >> 2 & 3; };
-    auto put_x = [&](const H& d, int part) {
+    auto mix = [](int row) { return SLOTS < 16 ? row >> 1 & 7 : MT <= 4 ? 4 * row : row & 15; };
+    auto put_x = [&](const H& d) {
 #pragma unroll
-        for (int i = 0; i < MB; ++i)
-#pragma unroll
-            for (int q = 0; q < H::PIECES; ++q) {
-                const int row = STEP * q + lane / PER, slot = lane % PER - part * SLOTS;
-                if (SPLIT == 1 || (slot >= 0 && slot < SLOTS)) own.x[(16 * i + row) * SLOTS + (slot ^ mix(row))] = d.x[i][q];
-            }
-    };
-    // The last chunk, which ends inside, straight to LDS (the scales of its blocks
-    // to `d`): what is past the row's end is zero.
-    const int left = int(a.k - whole * kChunk);                 // columns of it
-    auto put_partial = [&](H& d, int part) {
-        const uint8_t* codes = a.codes + n0 * a.ldc + whole * (kChunk / 2);
-        if (part == 0)
-#pragma unroll 1
-            for (int i = 0; i < NB; ++i) {
-                u32x4 v = {0, 0, 0, 0};
-                if (16 * i + (lane >> 2) < rows_n && 16 * (lane & 3) < (left + 1) / 2)
-                    v = *reinterpret_cast<const u32x4*>(codes + 16 * i * a.ldc + code_at);
-                own.codes[64 * i + (lane & ~3) + ((lane & 3) ^ (lane >> 4))] = v;
-            }
-        const uint8_t* x = static_cast<const uint8_t*>(a.x) + (m0 * a.ldx + whole * kChunk) * ES;
-#pragma unroll 1
-        for (int e = lane; e < 16 * MB * (PART / ES); e += 64) {
-            const int row = e / (PART / ES), byte = e % (PART / ES) * ES, k = part * (PART / ES) + e % (PART / ES);
-            uint8_t* to = reinterpret_cast<uint8_t*>(&own.x[row * SLOTS + (byte / 16 ^ mix(row))]) + byte % 16;
-            const bool in = row < rows_m && k < left;
-            if constexpr (EIGHT) *to = in ? x[row * a.ldx + k] : 0;
-            else *reinterpret_cast<uint16_t*>(to) = in ? reinterpret_cast<const uint16_t*>(x)[row * a.ldx + k] : 0;
-        }
-        if constexpr (XT == X::F8_BLOCK) {
-#pragma unroll
-            for (int i = 0; i < MB; ++i) {
-                uint32_t v = 0x7f7f7f7fu;
-                if (part == 0 && 16 * i + r < rows_m) {
-                    const uint8_t* p = static_cast<const uint8_t*>(a.xscales) + (m0 + 16 * i + r) * a.ldxs + whole * 4;
-#pragma unroll 1
-                    for (int j = 0; j * kScaleBlock < left; ++j) v = (v & ~(255u << (8 * j))) | uint32_t(p[j]) << (8 * j);
-                }
-                if (part == 0) d.xscale[i] = v;
-            }
+        for (int q = 0; q < H::PIECES; ++q) {
+            const int row = STEP * q + lane / PER;
+            if (H::BYTES >= 1024 || row < MT) own.x[row * SLOTS + (lane % PER ^ mix(row))] = MIXED ? mixed<EIGHT>(d.x[q]) : d.x[q];
         }
     };
     // Codes of product t for row lane % 16 of W: dword 4 t + lane / 16 of the row.
@@ -284,8 +306,8 @@ __global__ __launch_bounds__(64 * kWaves) void weight_matvec_kernel(MatvecArgs a
     };
     // Columns 32 t + 8 g of row lane % 16 of x.
     auto get_x = [&](int i, int t, [[maybe_unused]] uint32_t scale) {
-        const int byte = (32 * t + 8 * g) * ES % PART;
-        const uint32_t* p = reinterpret_cast<const uint32_t*>(&own.x[(16 * i + r) * SLOTS + (byte / 16 ^ mix(r))]);
+        const int row = 16 * i + (MT < 16 ? r % MT : r), byte = (32 * t + 8 * g) * ES;
+        const uint32_t* p = reinterpret_cast<const uint32_t*>(&own.x[row * SLOTS + (byte / 16 ^ mix(row))]);
         if constexpr (EIGHT) {
             const uint2 v = reinterpret_cast<const uint2*>(p)[g & 1];
             return from_e4m3<HALF>(v.x, v.y, XT == X::F8_BLOCK ? power_of(scale >> (8 * t) & 255u) : 1.0f);
@@ -300,20 +322,16 @@ __global__ __launch_bounds__(64 * kWaves) void weight_matvec_kernel(MatvecArgs a
 #pragma unroll
         for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 
-    // Multiplies chunk c, which is held if it lies inside the row, and loads chunk
-    // `next` if that does; `group`: its first group, of those staged.
-    auto multiply = [&](H& d, int64_t c, int group, int64_t next) {
+    // Multiplies the chunk that is held, and loads chunk `next` if it is before
+    // `full`; `group`: the first group of the one that is held, of those staged.
+    auto multiply = [&](H& d, int group, int next, int full) {
         wave_lds_sync();                                        // the last chunk has been read
-        if (c < whole) {
-            put_codes(d);
-            put_x(d, 0);
-        } else {
-            put_partial(d, 0);
-        }
+        put_codes(d);
+        put_x(d);
         uint32_t xscale[MB];
 #pragma unroll
         for (int i = 0; i < MB; ++i) xscale[i] = XT == X::F8_BLOCK ? d.xscale[i] : 0;
-        if (SPLIT == 1 && next < whole) load(next, d);
+        if (next < full) load(next, d);
         wave_lds_sync();
 #pragma unroll
         for (int s = 0; s < GROUPS; ++s) {
@@ -334,24 +352,17 @@ __global__ __launch_bounds__(64 * kWaves) void weight_matvec_kernel(MatvecArgs a
 #pragma unroll
             for (int q = 0; q < STEPS; ++q) {
                 const int t = s * STEPS + q;
-                if (SPLIT == 2 && t == 2) {
-                    wave_lds_sync();
-                    if (c < whole) put_x(d, 1);
-                    else put_partial(d, 1);
-                    if (next < whole) load(next, d);
-                    wave_lds_sync();
-                }
                 Frag x[MB];
 #pragma unroll
                 for (int i = 0; i < MB; ++i) {
                     x[i] = get_x(i, t, xscale[i]);
                     if constexpr (OFFSET)
-                        ones[i] = product<HALF>(x[i], Frag{{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u}}, ones[i]);
+                        ones[i] = product<HALF>(x[i], HALF ? Frag{{0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u}}
+                                                           : Frag{{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u}}, ones[i]);
                 }
 #pragma unroll
                 for (int j = 0; j < NB; ++j) {
-                    const f16 z = f16(zero[j]);
-                    const Frag w = unpack<HALF, F>(get_codes(j, t), f16x2{z, z});
+                    const Frag w = unpack<HALF, F, MIXED>(get_codes(j, t));
 #pragma unroll
                     for (int i = 0; i < MB; ++i) part[i][j] = product<HALF>(x[i], w, part[i][j]);
                 }
@@ -361,7 +372,7 @@ __global__ __launch_bounds__(64 * kWaves) void weight_matvec_kernel(MatvecArgs a
 #pragma unroll
                 for (int i = 0; i < MB; ++i)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
+                    for (int e = 0; e < SUMS; ++e) {
                         const float p = OFFSET ? fmadd(-zero[j], ones[i][e], part[i][j][e]) : part[i][j][e];
                         acc[i][j][e] = fmadd(scale[j], p, acc[i][j][e]);
                     }
@@ -371,15 +382,19 @@ __global__ __launch_bounds__(64 * kWaves) void weight_matvec_kernel(MatvecArgs a
 
     constexpr int PHASE = kGroups / GROUPS;                     // chunks whose scales fit
     H held = {};
-    for (int64_t base = 0; base < chunks; base += PHASE) {
-        const int64_t end = base + PHASE < chunks ? base + PHASE : chunks;
-        int64_t c = base + wave;
-        if (c < end && c < whole) load(c, held);                // on its way while the scales are staged
-        const int64_t g0 = base * GROUPS;
+    for (int base = 0; base < chunks; base += PHASE) {
+        const int end = base + PHASE < chunks ? base + PHASE : chunks;
+        const int full = end < whole ? end : whole;             // of them, those that lie inside the row
+        int c = base + wave;
+        if (c < full) load(c, held);                            // on its way while the scales are staged
+        const int g0 = base * GROUPS;
         if (base) __syncthreads();
-        stage(g0, int(end * GROUPS < groups ? end * GROUPS - g0 : groups - g0));
+        stage(g0, end * GROUPS < groups ? end * GROUPS - g0 : groups - g0);
         __syncthreads();
-        for (; c < end; c += waves) multiply(held, c, int(c - base) * GROUPS, c + waves < end ? c + waves : whole);
+        for (; c < end; c += waves) {
+            if (c >= whole) load_partial(held);
+            multiply(held, (c - base) * GROUPS, c + waves, full);
+        }
     }
 
     __syncthreads();                                            // the chunks' LDS is free
@@ -388,7 +403,7 @@ __global__ __launch_bounds__(64 * kWaves) void weight_matvec_kernel(MatvecArgs a
 #pragma unroll
         for (int j = 0; j < NB; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) lds.sums[wave][(i * NB + j) * 4 + e][lane] = acc[i][j][e];
+            for (int e = 0; e < SUMS; ++e) lds.sums[wave][(i * NB + j) * 4 + e][lane] = acc[i][j][e];
     __syncthreads();
 
     // whole wavefronts: the detour below takes all lanes
@@ -418,16 +433,22 @@ __global__ __launch_bounds__(64 * kWaves) void weight_matvec_kernel(MatvecArgs a
 template <X XT>
 inline hipError_t weight_matvec_t(Type yt, Format f, int group, const MatvecArgs& a, hipStream_t s) {
     const int64_t chunks = (a.k + kChunk - 1) / kChunk;
-    const dim3 block(uint32_t(64 * (chunks < kWaves ? chunks : kWaves)));
-    auto tile = [&](auto fmt, auto size, auto mb, auto nb) {
-        constexpr int MB = decltype(mb)::value, NB = decltype(nb)::value;
-        const dim3 grid(uint32_t((a.n + 16 * NB - 1) / (16 * NB)), uint32_t((a.m + 16 * MB - 1) / (16 * MB)));
-        return launch(weight_matvec_kernel<XT, decltype(fmt)::value, decltype(size)::value, MB, NB>, grid, block, 0, s, a, yt);
+    auto tile = [&](auto fmt, auto size, auto mt, auto nb, auto waves) {
+        constexpr int MT = decltype(mt)::value, NB = decltype(nb)::value, WAVES = decltype(waves)::value;
+        const dim3 block(uint32_t(64 * (chunks < WAVES ? chunks : WAVES)));
+        const dim3 grid(uint32_t((a.n + 16 * NB - 1) / (16 * NB)), uint32_t((a.m + MT - 1) / MT));
+        return launch(weight_matvec_kernel<XT, decltype(fmt)::value, decltype(size)::value, MT, NB, WAVES>, grid, block, 0, s,
+                      a, yt);
     };
+    constexpr int FEW = is_eight(XT) ? 8 : 4;                   // rows that one load holds
     auto shape = [&](auto fmt, auto size) {
         const bool wide = a.n >= 256 * 32;                      // enough rows for every compute unit at 32 each
-        if (a.m <= 16) return wide ? tile(fmt, size, ic<1>{}, ic<2>{}) : tile(fmt, size, ic<1>{}, ic<1>{});
-        return wide ? tile(fmt, size, ic<2>{}, ic<2>{}) : tile(fmt, size, ic<2>{}, ic<1>{});
+        auto rows = [&](auto mt) {
+            if (wide) return tile(fmt, size, mt, ic<2>{}, ic<8>{});
+            if (a.n <= 256 * 16) return tile(fmt, size, mt, ic<1>{}, ic<decltype(mt)::value <= 16 ? 16 : 8>{});
+            return tile(fmt, size, mt, ic<1>{}, ic<8>{});
+        };
+        return a.m == 1 ? rows(ic<1>{}) : a.m <= FEW ? rows(ic<FEW>{}) : a.m <= 16 ? rows(ic<16>{}) : rows(ic<32>{});
     };
     if (f == Format::FLOAT) return shape(std::integral_constant<Format, Format::FLOAT>{}, ic<32>{});
     using I = std::integral_constant<Format, Format::INTEGER>;
