@@ -142,14 +142,29 @@ __global__ __launch_bounds__(Shape<TPR>::threads) void rmsnorm_grad_kernel(NormG
 #pragma unroll
         for (int j = 0; j < 8; ++j) part[i][j] = 0;
     }
-    for (int64_t row = first; row < a.rows; row += int64_t(gridDim.x) * S::rows) {
-        Raw8<T> hr[VPT], gr[VPT];
+    const int64_t step = int64_t(gridDim.x) * S::rows;
+    constexpr bool AHEAD = VPT * sizeof(T) <= 8;                // the next row is on its way, if there is room
+    Raw8<T> hn[VPT], gn[VPT], en[VPT];
+    auto load = [&](int64_t row) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int c = 8 * (i * TPR + t), left = n - c;
+            hn[i] = load8(static_cast<const T*>(a.h) + row * a.ldh + c, left);
+            gn[i] = load8(static_cast<const T*>(a.dy) + row * a.lddy + c, left);
+            if (a.dh) en[i] = load8(static_cast<const T*>(a.dh) + row * a.lddh + c, left);
+        }
+    };
+    if (AHEAD && first < a.rows) load(first);
+    for (int64_t row = first; row < a.rows; row += step) {
+        if (!AHEAD) load(row);
+        Raw8<T> hr[VPT], gr[VPT], er[VPT];
         float square = 0, dot = 0;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int c = 8 * (i * TPR + t), left = n - c;
-            hr[i] = load8(static_cast<const T*>(a.h) + row * a.ldh + c, left);
-            gr[i] = load8(static_cast<const T*>(a.dy) + row * a.lddy + c, left);
+            hr[i] = hn[i];
+            gr[i] = gn[i];
+            er[i] = en[i];
             const Raw8<T> wr = KEEP ? kept[KEEP ? i : 0] : load8(w + c, left);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -158,6 +173,7 @@ __global__ __launch_bounds__(Shape<TPR>::threads) void rmsnorm_grad_kernel(NormG
                 dot = fmadd(gr[i][j] * wr[j], h, dot);
             }
         }
+        if (AHEAD && row + step < a.rows) load(row + step);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             hr[i].keep_packed();
@@ -205,9 +221,8 @@ __global__ __launch_bounds__(Shape<TPR>::threads) void rmsnorm_grad_kernel(NormG
                 part[i][j] = fmadd(g, unit, part[i][j]);
             }
             if (a.dh) {
-                const Raw8<T> er = load8(static_cast<const T*>(a.dh) + row * a.lddh + c, left);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) d[j] += er[j];
+                for (int j = 0; j < 8; ++j) d[j] += er[i][j];
             }
             store8(static_cast<T*>(a.dx) + row * a.lddx + c, d, left);
         }
@@ -230,8 +245,17 @@ static __global__ __launch_bounds__(256) void rmsnorm_dw_kernel(const float* par
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + x;
     float sum = 0;
-    if (c < n)
-        for (int64_t p = y; p < count; p += 8) sum += partial[p * n + c];
+    if (c < n) {
+        int64_t p = y;
+        for (; p + 56 < count; p += 64) {                       // eight loads on their way at a time
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = partial[(p + 8 * i) * n + c];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum += v[i];
+        }
+        for (; p < count; p += 8) sum += partial[p * n + c];
+    }
     slice[y][x] = sum;
     __syncthreads();
     if (y == 0 && c < n) {
@@ -288,10 +312,11 @@ inline hipError_t rmsnorm_quant_t(Scale sc, const NormQuantArgs& a, hipStream_t 
     });
 }
 
-// Workgroups of the gradient kernel.
+// Workgroups of the gradient kernel: two a compute unit, and not less than four
+// rows each, whose sums of dw are then fewer.
 template <int TPR>
 inline int64_t grad_groups(int64_t rows) {
-    const int64_t need = (rows + Shape<TPR>::rows - 1) / Shape<TPR>::rows;
+    const int64_t need = (rows + 4 * Shape<TPR>::rows - 1) / (4 * Shape<TPR>::rows);
     const int64_t most = 512;
     return need < most ? need : most;
 }

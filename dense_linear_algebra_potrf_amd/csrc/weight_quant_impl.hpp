@@ -33,14 +33,13 @@ __device__ __forceinline__ float e2m1_value(uint32_t code) {
 }
 
 template <typename T, Format F, int GROUP, bool ZEROS>
-__global__ __launch_bounds__(256) void weight_quant_kernel(WeightQuantArgs a) {
+__global__ __launch_bounds__(256) void weight_quant_kernel(WeightQuantArgs a, int across) {
     constexpr int LANES = GROUP / 8;
-    const int64_t per_row = (a.k + 127) / 128 * 16;           // threads of a row: whole DPP rows
-    const int64_t total = a.n * per_row;
-    for (int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x; id < total; id += int64_t(gridDim.x) * 256) {
-        const int64_t row = id / per_row;
-        const int c = int(id - row * per_row) * 8;
-        const int left = int(a.k) - c;
+    // 2^across threads along a row, at least a DPP row's 16; the others down the rows
+    const int64_t step = int64_t(gridDim.y) << (8 - across);
+    const int c = int((blockIdx.x << across) + (threadIdx.x & ((1 << across) - 1))) * 8;
+    const int left = int(a.k) - c;
+    for (int64_t row = (int64_t(blockIdx.y) << (8 - across)) + (threadIdx.x >> across); row < a.n; row += step) {
         const Raw8<T> wr = load8(static_cast<const T*>(a.W) + row * a.ldw + c, left);
         float w[8], value[8];
         uint32_t top = 0;
@@ -113,12 +112,14 @@ __global__ __launch_bounds__(256) void weight_quant_kernel(WeightQuantArgs a) {
 
 template <typename T>
 inline hipError_t weight_quant_t(Format f, int group, const WeightQuantArgs& a, hipStream_t s) {
-    const int64_t need = (a.n * ((a.k + 127) / 128 * 16) + 255) / 256;
-    const int64_t most = 1 << 20;
-    const dim3 grid(uint32_t(need < most ? need : most)), block(256);
+    const int64_t threads = (a.k + 7) / 8;                     // of a row
+    int across = 4;
+    while (across < 8 && (1 << across) < threads) ++across;
+    const int64_t down = (a.n + (256 >> across) - 1) >> (8 - across);
+    const dim3 grid(uint32_t((threads + (1 << across) - 1) >> across), uint32_t(down < 65535 ? down : 65535)), block(256);
     auto go = [&](auto fmt, auto size, auto zeros) {
         return launch(weight_quant_kernel<T, decltype(fmt)::value, decltype(size)::value, decltype(zeros)::value>,
-                      grid, block, 0, s, a);
+                      grid, block, 0, s, a, across);
     };
     using I = std::integral_constant<Format, Format::INTEGER>;
     if (f == Format::FLOAT) return go(std::integral_constant<Format, Format::FLOAT>{}, ic<32>{}, std::false_type{});

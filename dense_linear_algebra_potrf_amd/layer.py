@@ -14,7 +14,6 @@ _FORMATS = {"int4": 0, "fp4": 1}
 _SCALES = {"row": 1, "block": 2}
 _E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
 
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _lib = _check = None
 
 
@@ -28,29 +27,28 @@ def _bind():
 
 
 def _rows(t, name: str, dtype=None, shape=None):
-    """(rows, columns, row stride) of a GPU tensor, taken as a matrix of its last dimension."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must live on the GPU")
+    """(rows, columns, row stride) of a tensor, taken as a matrix of its last dimension."""
     if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.dim() == 2:
-        rows, n = t.shape
-        ld = t.stride(0) if rows > 1 else n
-        if n > 1 and t.stride(1) != 1:
+    size = t.shape
+    if len(size) == 2:
+        rows, n = size
+        ld, step = t.stride()
+        if step != 1 and n > 1:
             raise ValueError(f"{name} must have contiguous rows")
+        if rows <= 1:
+            ld = n
     else:
-        if t.dim() < 1 or not t.is_contiguous():
+        if not size or not t.is_contiguous():
             raise ValueError(f"{name} must be a matrix, or contiguous")
-        n = ld = t.shape[-1]
+        n = ld = size[-1]
         rows = t.numel() // n if n else 0
-    if shape is not None and shape != (rows, n):
+    if shape is not None and (shape[0] != rows or shape[1] != n):
         raise ValueError(f"{name} must be {shape[0]} x {shape[1]}, not {rows} x {n}")
     return rows, n, ld
 
 
 def _vector(t, name: str, dtype, n: int) -> int:
-    if not t.is_cuda:
-        raise ValueError(f"{name} must live on the GPU")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     if t.numel() != n or not t.is_contiguous():
@@ -58,17 +56,24 @@ def _vector(t, name: str, dtype, n: int) -> int:
     return t.data_ptr()
 
 
-def _place(t, others, stream) -> int:
-    """The stream's handle, after checking that every tensor is on the current device."""
+def _gpu(t) -> int:
+    """The index of the GPU that t is on."""
     at = t.get_device()
-    if at != torch.cuda.current_device():
-        raise ValueError("tensors must live on the current device")
+    if at < 0:
+        raise ValueError("tensors must live on the GPU")
+    return at
+
+
+def _place(at: int, others, stream) -> int:
+    """The stream's handle, after checking that every tensor is on the current device, `at`."""
     for o in others:
         if o is not None and o.get_device() != at:
-            raise ValueError("tensors must live on one device")
+            raise ValueError("tensors must live on the GPU, on one device")
+    if at != torch._C._cuda_getDevice():
+        raise ValueError("tensors must live on the current device")
     if stream is not None:
         return int(stream.cuda_stream)
-    return _raw_stream(at) if _raw_stream else int(torch.cuda.current_stream().cuda_stream)
+    return torch._C._cuda_getCurrentRawStream(at)
 
 
 def _float_type(t, name: str) -> int:
@@ -89,6 +94,7 @@ def rmsnorm_quant(x, weight, residual=None, *, eps: float = 1e-6, scale: str = "
     """
     lib = _lib or _bind()
     ty = _float_type(x, "x")
+    at = _gpu(x)
     rows, n, ldx = _rows(x, "x")
     dt, dev = x.dtype, x.device
     w = _vector(weight, "weight", dt, n)
@@ -117,7 +123,7 @@ def rmsnorm_quant(x, weight, residual=None, *, eps: float = 1e-6, scale: str = "
         if scales is None:
             scales = torch.empty(rows, dtype=torch.float32, device=dev)
         _vector(scales, "scales", torch.float32, rows)
-    s = _place(x, (weight, residual, residual_out, out, scales), stream)
+    s = _place(at, (weight, residual, residual_out, out, scales), stream)
     st = lib.batchlas_rmsnorm_quant(ty, _SCALES[scale], rows, n, x.data_ptr(), ldx, rp, ldr, w, eps,
                                     hp, ldh, out.data_ptr(), ldq, scales.data_ptr(), lds, s)
     if st:
@@ -137,6 +143,7 @@ def rmsnorm_grad(dy, h, weight, dh=None, *, eps: float = 1e-6, dx=None, dweight=
     """
     lib = _lib or _bind()
     ty = _float_type(h, "h")
+    at = _gpu(h)
     rows, n, ldh = _rows(h, "h")
     dt, dev = h.dtype, h.device
     lddy = _rows(dy, "dy", dt, (rows, n))[2]
@@ -157,7 +164,7 @@ def rmsnorm_grad(dy, h, weight, dh=None, *, eps: float = 1e-6, dx=None, dweight=
         if workspace is not None:
             size = workspace.numel()
             wp = _vector(workspace, "workspace", torch.uint8, size)
-    s = _place(h, (dy, weight, dh, dx, dweight if dp else None, workspace if wp else None), stream)
+    s = _place(at, (dy, weight, dh, dx, dweight if dp else None, workspace if wp else None), stream)
     st = lib.batchlas_rmsnorm_grad(ty, rows, n, dy.data_ptr(), lddy, h.data_ptr(), ldh, w,
                                    None if dh is None else dh.data_ptr(), lddh, eps, dx.data_ptr(), lddx,
                                    dp, wp, size, s)
@@ -205,6 +212,7 @@ def weight_quant(W, *, format: str = "int4", group: int | None = None, zeros: bo
     """
     lib = _lib or _bind()
     ty = _float_type(W, "W")
+    at = _gpu(W)
     n, k, ldw = _rows(W, "W")
     dev = W.device
     st_type = _scale_type(format)
@@ -237,7 +245,7 @@ def weight_quant(W, *, format: str = "int4", group: int | None = None, zeros: bo
     if values is not None:
         ldv = _rows(values, "values", W.dtype, (n, k))[2]
         vp = values.data_ptr()
-    s = _place(W, (codes, scales, zeros_out, values), stream)
+    s = _place(at, (codes, scales, zeros_out, values), stream)
     st = lib.batchlas_weight_quant(ty, _FORMATS[format], group, n, k, W.data_ptr(), ldw, codes.data_ptr(), ldc,
                                    scales.data_ptr(), lds, zp, ldz, vp, ldv, s)
     if st:
@@ -257,6 +265,7 @@ def weight_matvec(x, codes, scales, zeros=None, *, format: str = "int4", group: 
     xt = _TYPES.get(x.dtype, -1)
     if xt < 1:
         raise TypeError(f"x must be bfloat16, float16 or float8_e4m3fn, not {x.dtype}")
+    at = _gpu(x)
     m, k, ldx = _rows(x, "x")
     st_type = _scale_type(format)
     if group is None:
@@ -286,7 +295,7 @@ def weight_matvec(x, codes, scales, zeros=None, *, format: str = "int4", group: 
         out = torch.empty((*x.shape[:-1], n), dtype=out_dtype, device=x.device)
     yt = _float_type(out, "out")
     ldy = _rows(out, "out", out_dtype, (m, n))[2]
-    s = _place(x, (codes, scales, zeros, x_scales, out), stream)
+    s = _place(at, (codes, scales, zeros, x_scales, out), stream)
     st = lib.batchlas_weight_matvec(xt, xs, yt, _FORMATS[format], group, m, n, k, x.data_ptr(), ldx, xp, ldxs,
                                     codes.data_ptr(), ldc, scales.data_ptr(), lds, zp, ldz, out.data_ptr(), ldy, s)
     if st:

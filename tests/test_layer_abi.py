@@ -80,7 +80,8 @@ def test_rmsnorm_grad_workspace(lib):
     assert lib.batchlas_rmsnorm_grad_workspace(2, 1, 100, ctypes.byref(size)) == 0 and size.value == 0
     for rows, n in ((2, 1), (517, 1537), (1 << 20, 4096), (3, 16384)):
         assert lib.batchlas_rmsnorm_grad_workspace(1, rows, n, ctypes.byref(size)) == 0
-        assert size.value % (4 * n) == 0 and 4 * n <= size.value <= 4 * n * min(4 * rows, 4096)
+        # whole rows of partial sums, or none where one workgroup sums all rows
+        assert size.value % (4 * n) == 0 and 0 <= size.value <= 4 * n * min(4 * rows, 4096)
     assert lib.batchlas_rmsnorm_grad_workspace(1, 4, 16385, ctypes.byref(size)) == 3
     assert lib.batchlas_rmsnorm_grad_workspace(3, 4, 64, ctypes.byref(size)) == 1
     assert lib.batchlas_rmsnorm_grad_workspace(1, 4, 64, None) == 2
