@@ -34,7 +34,7 @@ EXPORTS = [
     "batchlas_sposv", "batchlas_dposv", "batchlas_cposv", "batchlas_zposv",
     "batchlas_route", "batchlas_status_string", "batchlas_last_error", "batchlas_version",
     "batchlas_rmsnorm_quant", "batchlas_rmsnorm_grad", "batchlas_rmsnorm_grad_workspace",
-    "batchlas_weight_quant", "batchlas_weight_matvec",
+    "batchlas_weight_quant", "batchlas_weight_matvec", "batchlas_weight_matvec_workspace",
 ]
 
 
@@ -99,11 +99,13 @@ def load_library():
         lib.batchlas_weight_quant.argtypes = [i32, i32, i64, i64, i64, vp, i64, vp, i64, vp, i64, vp,
                                               i64, vp, i64, vp]
         lib.batchlas_weight_matvec.argtypes = [i32, i32, i32, i32, i64, i64, i64, i64, vp, i64, vp, i64,
-                                               vp, i64, vp, i64, vp, i64, vp, i64, vp]
+                                               vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp]
+        lib.batchlas_weight_matvec_workspace.argtypes = [i64, i64, ctypes.POINTER(i64)]
         for name in ("batchlas_potrf", "batchlas_posv", "batchlas_potrf_family",
                      "batchlas_posv_family", "batchlas_route", "batchlas_rmsnorm_quant",
                      "batchlas_rmsnorm_grad", "batchlas_rmsnorm_grad_workspace",
-                     "batchlas_weight_quant", "batchlas_weight_matvec"):
+                     "batchlas_weight_quant", "batchlas_weight_matvec",
+                     "batchlas_weight_matvec_workspace"):
             getattr(lib, name).restype = i32
         lib.batchlas_status_string.argtypes = [i32]
         lib.batchlas_status_string.restype = ctypes.c_char_p
@@ -227,7 +229,7 @@ def version() -> int:
 # ---------------------------------------------------------------- low-bit layer operators
 # In modules of their own, which import torch; loaded at first use.
 _LAZY = {"rmsnorm_quant": "layer", "rmsnorm_grad": "layer", "rmsnorm_grad_workspace": "layer",
-         "weight_quant": "layer", "weight_matvec": "layer"}
+         "weight_quant": "layer", "weight_matvec": "layer", "weight_matvec_workspace": "layer"}
 
 
 def __getattr__(name: str):

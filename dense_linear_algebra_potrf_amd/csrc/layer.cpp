@@ -196,8 +196,20 @@ batchlas_status do_weight_quant(int type, int format, int64_t group, const bl::W
                           "weight_quant launch");
 }
 
+batchlas_status matvec_bytes(int64_t m, int64_t k, int64_t& bytes) {
+    BL_REQUIRE(m >= 0, "m must be >= 0");
+    BL_REQUIRE(k >= 1, "k must be >= 1");
+    BL_REQUIRE(m < kMost && k <= kMost / 2, "m or k is out of range");
+    if (m > (int64_t(1) << 21)) return fail(BATCHLAS_NOT_SUPPORTED, "m is beyond 2^21");
+    const int64_t need = bl::weight_matvec_workspace(m, k);
+    if (need > (int64_t(1) << 35)) return fail(BATCHLAS_NOT_SUPPORTED, "m * k is beyond 2^34");
+    bytes = need;
+    return BATCHLAS_OK;
+}
+
 batchlas_status do_weight_matvec(int xtype, int xscale, int ytype, int format, int64_t group,
-                                 const bl::MatvecArgs& a, hipStream_t stream) {
+                                 const bl::MatvecArgs& a, void* workspace, int64_t bytes,
+                                 hipStream_t stream) {
     const bool eight = xtype == BATCHLAS_TYPE_E4M3;
     BL_REQUIRE(eight || xtype == BATCHLAS_TYPE_F16 || xtype == BATCHLAS_TYPE_BF16,
                "xtype must be F16, BF16 or E4M3");
@@ -228,23 +240,29 @@ batchlas_status do_weight_matvec(int xtype, int xscale, int ytype, int format, i
         BL_POINTER(a.y, "y");
     }
     BL_REQUIRE(aligned(a.codes, 16), "codes must be aligned to 16 bytes");
+    BL_REQUIRE(aligned(workspace, 16), "workspace must be aligned to 16 bytes");
     BL_REQUIRE(aligned(a.x, size_of(xtype)) && aligned(a.y, size_of(ytype)) &&
                    (block || aligned(a.xscales, 4)) &&
                    (format == BATCHLAS_FORMAT_FLOAT || aligned(a.scales, 2)),
                "an array is not aligned to its element size");
-    if (a.m > (int64_t(1) << 21))
-        return fail(BATCHLAS_NOT_SUPPORTED, "m is beyond 2^21");
+    int64_t need = 0;
+    st = matvec_bytes(a.m, a.k, need);
+    if (st != BATCHLAS_OK) return st;
     if (a.n > (int64_t(1) << 24))
         return fail(BATCHLAS_NOT_SUPPORTED, "n is beyond 2^24");
     // offsets within a tile of rows are 32-bit
     if (a.ldx > (int64_t(1) << 27) || a.ldc > (int64_t(1) << 27))
         return fail(BATCHLAS_NOT_SUPPORTED, "ldx or ldc is beyond 2^27");
     if (a.m == 0) return BATCHLAS_OK;
+    if (need) {
+        BL_POINTER(workspace, "workspace");
+        BL_REQUIRE(bytes >= need, "workspace_bytes is less than weight_matvec_workspace gives");
+    }
     st = bl::check_device();
     if (st != BATCHLAS_OK) return st;
     return bl::hip_status(bl::weight_matvec(static_cast<Type>(xtype), static_cast<Scale>(xscale),
                                             static_cast<Type>(ytype), static_cast<Format>(format),
-                                            int(group), a, stream),
+                                            int(group), a, workspace, stream),
                           "weight_matvec launch");
 }
 
@@ -303,12 +321,20 @@ batchlas_status batchlas_weight_matvec(batchlas_type xtype, batchlas_scale xscal
                                        int64_t ldx, const void* xscales, int64_t ldxs,
                                        const uint8_t* codes, int64_t ldc, const void* scales,
                                        int64_t lds, const uint8_t* zeros, int64_t ldz, void* y,
-                                       int64_t ldy, batchlas_stream_t stream) {
+                                       int64_t ldy, void* workspace, int64_t workspace_bytes,
+                                       batchlas_stream_t stream) {
     return guarded([&] {
         return do_weight_matvec(xtype, xscale, ytype, format, group,
                                 {m, n, k, x, ldx, xscales, ldxs, codes, ldc, scales, lds, zeros,
                                  ldz, y, ldy},
-                                reinterpret_cast<hipStream_t>(stream));
+                                workspace, workspace_bytes, reinterpret_cast<hipStream_t>(stream));
+    });
+}
+
+batchlas_status batchlas_weight_matvec_workspace(int64_t m, int64_t k, int64_t* bytes) {
+    return guarded([&]() -> batchlas_status {
+        BL_POINTER(bytes, "bytes");
+        return matvec_bytes(m, k, *bytes);
     });
 }
 

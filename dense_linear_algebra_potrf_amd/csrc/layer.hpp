@@ -62,7 +62,9 @@ struct MatvecArgs {
     const uint8_t* zeros; int64_t ldz;   // may be null
     void* y; int64_t ldy;
 };
-hipError_t weight_matvec(Type xt, Scale xs, Type yt, Format f, int group, const MatvecArgs& a,
+constexpr int64_t kFewRows = 16;         // above it x is laid out anew in the workspace first
+int64_t weight_matvec_workspace(int64_t m, int64_t k);    // bytes
+hipError_t weight_matvec(Type xt, Scale xs, Type yt, Format f, int group, const MatvecArgs& a, void* workspace,
                          hipStream_t s);
 
 }  // namespace bl

@@ -56,6 +56,12 @@ __device__ __forceinline__ f32x4 product(const Frag& a, const Frag& b, f32x4 c) 
 }
 
 template <bool HALF>
+__device__ __forceinline__ Frag ones_of() {
+    constexpr uint32_t one = HALF ? 0x3c003c00u : 0x3f803f80u;
+    return Frag{{one, one, one, one}};
+}
+
+template <bool HALF>
 __device__ __forceinline__ Frag from_e4m3(uint32_t lo, uint32_t hi, float scale) {
     Frag f;
     if constexpr (HALF) {
@@ -106,28 +112,27 @@ __device__ __forceinline__ u32x4 mixed(u32x4 v) {
     else return u32x4{perm(v[1], v[0], LO), perm(v[3], v[2], LO), perm(v[1], v[0], HI), perm(v[3], v[2], HI)};
 }
 
-// The first `bytes` (of elements of ES bytes) of 16 at p, the others zero.  Where
-// the row holds 16 bytes at least (is_long), one load of the 16 that end with them.
+// `bytes` (of elements of ES bytes) of 16 at p, the others zero: of a row that is
+// shorter than 16 bytes.
 template <int ES>
-__device__ __forceinline__ u32x4 load_start(const uint8_t* p, int bytes, bool is_long) {
-    using u64x2 = uint64_t __attribute__((ext_vector_type(2)));
-    u64x2 v = {0, 0};
-    if (bytes >= 16) {
-        __builtin_memcpy(&v, p, 16);
-    } else if (is_long) {
-        __builtin_memcpy(&v, p + bytes - 16, 16);
-        const int cut = 8 * (16 - bytes);                       // 8..120 bits
-        v = cut < 64 ? u64x2{v[0] >> cut | v[1] << (64 - cut), v[1] >> cut} : u64x2{v[1] >> (cut - 64), 0};
-    } else {
+__device__ __forceinline__ u32x4 load_short(const uint8_t* p, int bytes) {
+    uint64_t lo = 0, hi = 0;
 #pragma unroll 1
-        for (int j = 0; j < bytes; j += ES) {
-            uint64_t e = p[j];
-            if constexpr (ES == 2) e |= uint64_t(p[j + 1]) << 8;
-            if (j < 8) v[0] |= e << (8 * j);
-            else v[1] |= e << (8 * j - 64);
-        }
+    for (int j = 0; j < bytes; j += ES) {
+        uint64_t e = p[j];
+        if constexpr (ES == 2) e |= uint64_t(p[j + 1]) << 8;
+        if (j < 8) lo |= e << (8 * j);
+        else hi |= e << (8 * j - 64);
     }
-    return __builtin_bit_cast(u32x4, v);
+    return u32x4{uint32_t(lo), uint32_t(lo >> 32), uint32_t(hi), uint32_t(hi >> 32)};
+}
+// The last `bytes` of 16, moved to the front; zeros after them.
+__device__ __forceinline__ u32x4 to_front(u32x4 v, int bytes) {
+    const uint64_t lo = uint64_t(v[1]) << 32 | v[0], hi = uint64_t(v[3]) << 32 | v[2];
+    const int cut = 8 * (16 - bytes);                           // 0..120 bits
+    const uint64_t a = cut == 0 ? lo : cut < 64 ? lo >> cut | hi << (64 - cut) : hi >> (cut - 64);
+    const uint64_t b = cut < 64 ? hi >> cut : 0;
+    return u32x4{uint32_t(a), uint32_t(a >> 32), uint32_t(b), uint32_t(b >> 32)};
 }
 
 // What a lane loads of a chunk: 16 bytes of a row of W per 16 rows, and of x in
@@ -169,6 +174,71 @@ __device__ __forceinline__ double by_definition(const MatvecArgs& a, X xt, Forma
     return sum;
 }
 
+// Scales of `count` groups from `first` on, of the TILE rows of W from n0 on, to
+// LDS: a float's bits (FLOAT), or its upper half with the zero point in the lower.
+// Neighbouring lanes take neighbouring rows and 8 groups each, so that the writes
+// spread over the banks.  Groups that the last chunk lacks (a chunk has GROUPS)
+// get a finite scale; their products are zero.
+template <Format F, int GROUPS, int TILE>
+__device__ __forceinline__ void stage_scales(const MatvecArgs& a, int64_t n0, int first, int count, uint32_t (*scales)[TILE]) {
+    constexpr int SB = F == Format::FLOAT ? 1 : 2;              // bytes of a scale
+    const int rounded = (count + GROUPS - 1) / GROUPS * GROUPS;
+    for (int e = threadIdx.x; e < (rounded + 7) / 8 * TILE; e += blockDim.x) {
+        const int row = e % TILE, at = e / TILE * 8, left = count - at;
+        const int64_t n = n0 + row < a.n ? n0 + row : a.n - 1;
+        const uint8_t* p = static_cast<const uint8_t*>(a.scales) + (n * a.lds + first + at) * SB;
+        const uint8_t* q = a.zeros + n * a.ldz + first + at;
+        if (left >= 8) {
+            uint8_t s[8 * SB], z[8] = {8, 8, 8, 8, 8, 8, 8, 8};
+            __builtin_memcpy(s, p, sizeof(s));
+            if (SB == 2 && a.zeros) __builtin_memcpy(z, q, 8);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                scales[at + j][row] = SB == 1 ? __builtin_bit_cast(uint32_t, power_of(s[j]))
+                                              : uint32_t(s[j * SB + SB - 1]) << 24 | uint32_t(s[j * SB]) << 16 | z[j];
+        } else {
+#pragma unroll 1
+            for (int j = 0; j < 8 && at + j < rounded; ++j) {
+                uint32_t v = 0;
+                if (j < left)
+                    v = SB == 1 ? __builtin_bit_cast(uint32_t, power_of(p[j]))
+                                : uint32_t(p[j * SB + SB - 1]) << 24 | uint32_t(p[j * SB]) << 16 | (a.zeros ? q[j] : 8);
+                scales[at + j][row] = v;
+            }
+        }
+    }
+}
+
+// Joins the wavefronts' sums (slot of four rows by lane) and stores the tile's y.
+template <Format F, int GROUP, int MB, int NB>
+__device__ __forceinline__ void store_sums(const MatvecArgs& a, X xt, Type yt, int64_t m0, int64_t n0, int rows_m, int rows_n,
+                                           int waves, const float (*sums)[MB * NB * 4][64]) {
+    constexpr int TILE = 16 * NB;
+    const int lane = threadIdx.x & 63;
+    // whole wavefronts: the detour below takes all lanes
+    for (int e0 = threadIdx.x & ~63; e0 < rows_m * TILE; e0 += blockDim.x) {
+        const int e = e0 + lane, ml = e / TILE, nl = e % TILE;  // y's row and column in the tile
+        const int64_t m = m0 + ml, n = n0 + nl;
+        const bool in = ml < rows_m && nl < rows_n;
+        const int slot = (ml / 16 * NB + nl / 16) * 4 + ml % 4, from = ml % 16 / 4 * 16 + nl % 16;
+        float v = 0;
+        if (in) {
+            for (int w = 0; w < waves; ++w) v += sums[w][slot][from];
+            if (xt == X::F8_ROW) v *= static_cast<const float*>(a.xscales)[m];
+        }
+        for (uint64_t odd = __ballot(magnitude(v) >= kInfBits); odd; odd &= odd - 1) {
+            const int at = __builtin_ctzll(odd);
+            const double d = by_definition(a, xt, F, GROUP, m0 + (e0 + at) / TILE, n0 + (e0 + at) % TILE);
+            if (lane == at) v = float(d);
+        }
+        if (!in) continue;
+        const int64_t to = m * a.ldy + n;
+        if (yt == Type::F32) static_cast<float*>(a.y)[to] = v;
+        else if (yt == Type::F16) static_cast<f16*>(a.y)[to] = f16(v);
+        else static_cast<bf16*>(a.y)[to] = bf16(v);
+    }
+}
+
 template <X XT, Format F, int GROUP, int MT, int NB, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void weight_matvec_kernel(MatvecArgs a, Type yt) {
     constexpr bool HALF = in_half(XT), EIGHT = is_eight(XT);
@@ -178,7 +248,6 @@ __global__ __launch_bounds__(64 * WAVES) void weight_matvec_kernel(MatvecArgs a,
     constexpr int TILE = 16 * NB;                               // rows of W
     constexpr int ES = EIGHT ? 1 : 2, ROW = kChunk * ES;        // bytes of an element and a chunk's row of x
     constexpr int SLOTS = ROW / 16;                             // of 16 bytes
-    constexpr int SB = F == Format::FLOAT ? 1 : 2;              // bytes of a scale
     using H = Held<XT, MT, NB>;
     // integers come apart in a mixed order: x is mixed alike on its way into LDS,
     // or the codes on their way out of it, whichever is less
@@ -196,38 +265,6 @@ __global__ __launch_bounds__(64 * WAVES) void weight_matvec_kernel(MatvecArgs a,
     const int chunks = int((a.k + kChunk - 1) / kChunk), whole = int(a.k / kChunk);
     const int groups = int((a.k + GROUP - 1) / GROUP);
     const int rows_n = a.n - n0 < TILE ? int(a.n - n0) : TILE, rows_m = a.m - m0 < MT ? int(a.m - m0) : MT;
-
-    // Scales of the groups from `first` on, to LDS: a float's upper half and, for
-    // integers, the zero point in the lower.  Neighbouring lanes take neighbouring
-    // rows and 8 groups each, so that the writes spread over the banks.  Groups
-    // that the last chunk lacks get a finite scale; their products are zero.
-    auto stage = [&](int first, int count) {
-        const int rounded = (count + GROUPS - 1) / GROUPS * GROUPS;
-        for (int e = threadIdx.x; e < (rounded + 7) / 8 * TILE; e += blockDim.x) {
-            const int row = e % TILE, at = e / TILE * 8, left = count - at;
-            const int64_t n = n0 + row < a.n ? n0 + row : a.n - 1;
-            const uint8_t* p = static_cast<const uint8_t*>(a.scales) + (n * a.lds + first + at) * SB;
-            const uint8_t* q = a.zeros + n * a.ldz + first + at;
-            if (left >= 8) {
-                uint8_t s[8 * SB], z[8] = {8, 8, 8, 8, 8, 8, 8, 8};
-                __builtin_memcpy(s, p, sizeof(s));
-                if (SB == 2 && a.zeros) __builtin_memcpy(z, q, 8);
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    scales[at + j][row] = SB == 1 ? __builtin_bit_cast(uint32_t, power_of(s[j]))
-                                                  : uint32_t(s[j * SB + SB - 1]) << 24 | uint32_t(s[j * SB]) << 16 | z[j];
-            } else {
-#pragma unroll 1
-                for (int j = 0; j < 8 && at + j < rounded; ++j) {
-                    uint32_t v = 0;
-                    if (j < left)
-                        v = SB == 1 ? __builtin_bit_cast(uint32_t, power_of(p[j]))
-                                    : uint32_t(p[j * SB + SB - 1]) << 24 | uint32_t(p[j * SB]) << 16 | (a.zeros ? q[j] : 8);
-                    scales[at + j][row] = v;
-                }
-            }
-        }
-    };
 
     // Loads a chunk that lies inside the row.  Codes: lane / 4 is the row, lane % 4
     // the 16 bytes of it.  x: 64 / PER rows a load, PER lanes a row.  Rows past the
@@ -266,11 +303,20 @@ __global__ __launch_bounds__(64 * WAVES) void weight_matvec_kernel(MatvecArgs a,
                 d.codes[i] = *reinterpret_cast<const u32x4*>(codes + code_at);
         }
         const uint8_t* x = x0 + int64_t(whole) * ROW;
-        const int bytes = left * ES - 16 * (lane % PER);        // of this lane's piece
+        // of this lane's piece: a load of the 16 bytes that end with the row, if it has so many
+        const int left_here = left * ES - 16 * (lane % PER), bytes = left_here < 16 ? left_here : 16;
+        const bool is_long = a.k * ES >= 16;
 #pragma unroll
-        for (int q = 0; q < H::PIECES; ++q, x += x_step) {
+        for (int q = 0; q < H::PIECES; ++q) {
             d.x[q] = u32x4{0, 0, 0, 0};
-            if (STEP * q + lane / PER < rows_m && bytes > 0) d.x[q] = load_start<ES>(x + x_at, bytes, a.k * ES >= 16);
+            if (STEP * q + lane / PER < rows_m && bytes > 0) {
+                if (is_long) __builtin_memcpy(&d.x[q], x + q * x_step + x_at + bytes - 16, 16);
+                else d.x[q] = load_short<ES>(x + q * x_step + x_at, bytes);
+            }
+        }
+        if (is_long && bytes > 0) {
+#pragma unroll
+            for (int q = 0; q < H::PIECES; ++q) d.x[q] = to_front(d.x[q], bytes);
         }
         if constexpr (XT == X::F8_BLOCK) {
 #pragma unroll
@@ -357,8 +403,7 @@ __global__ __launch_bounds__(64 * WAVES) void weight_matvec_kernel(MatvecArgs a,
                 for (int i = 0; i < MB; ++i) {
                     x[i] = get_x(i, t, xscale[i]);
                     if constexpr (OFFSET)
-                        ones[i] = product<HALF>(x[i], HALF ? Frag{{0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u}}
-                                                           : Frag{{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u}}, ones[i]);
+                        ones[i] = product<HALF>(x[i], ones_of<HALF>(), ones[i]);
                 }
 #pragma unroll
                 for (int j = 0; j < NB; ++j) {
@@ -389,7 +434,7 @@ __global__ __launch_bounds__(64 * WAVES) void weight_matvec_kernel(MatvecArgs a,
         if (c < full) load(c, held);                            // on its way while the scales are staged
         const int g0 = base * GROUPS;
         if (base) __syncthreads();
-        stage(g0, end * GROUPS < groups ? end * GROUPS - g0 : groups - g0);
+        stage_scales<F, GROUPS, TILE>(a, n0, g0, end * GROUPS < groups ? end * GROUPS - g0 : groups - g0, scales);
         __syncthreads();
         for (; c < end; c += waves) {
             if (c >= whole) load_partial(held);
@@ -406,28 +451,7 @@ __global__ __launch_bounds__(64 * WAVES) void weight_matvec_kernel(MatvecArgs a,
             for (int e = 0; e < SUMS; ++e) lds.sums[wave][(i * NB + j) * 4 + e][lane] = acc[i][j][e];
     __syncthreads();
 
-    // whole wavefronts: the detour below takes all lanes
-    for (int e0 = threadIdx.x & ~63; e0 < rows_m * TILE; e0 += blockDim.x) {
-        const int e = e0 + lane, ml = e / TILE, nl = e % TILE;  // y's row and column in the tile
-        const int64_t m = m0 + ml, n = n0 + nl;
-        const bool in = ml < rows_m && nl < rows_n;
-        const int slot = (ml / 16 * NB + nl / 16) * 4 + ml % 4, from = ml % 16 / 4 * 16 + nl % 16;
-        float v = 0;
-        if (in) {
-            for (int w = 0; w < waves; ++w) v += lds.sums[w][slot][from];
-            if (XT == X::F8_ROW) v *= static_cast<const float*>(a.xscales)[m];
-        }
-        for (uint64_t odd = __ballot(magnitude(v) >= kInfBits); odd; odd &= odd - 1) {
-            const int at = __builtin_ctzll(odd);
-            const double d = by_definition(a, XT, F, GROUP, m0 + (e0 + at) / TILE, n0 + (e0 + at) % TILE);
-            if (lane == at) v = float(d);
-        }
-        if (!in) continue;
-        const int64_t to = m * a.ldy + n;
-        if (yt == Type::F32) static_cast<float*>(a.y)[to] = v;
-        else if (yt == Type::F16) static_cast<f16*>(a.y)[to] = f16(v);
-        else static_cast<bf16*>(a.y)[to] = bf16(v);
-    }
+    store_sums<F, GROUP, MB, NB>(a, XT, yt, m0, n0, rows_m, rows_n, waves, &lds.sums[0]);
 }
 
 template <X XT>
@@ -445,10 +469,10 @@ inline hipError_t weight_matvec_t(Type yt, Format f, int group, const MatvecArgs
         const bool wide = a.n >= 256 * 32;                      // enough rows for every compute unit at 32 each
         auto rows = [&](auto mt) {
             if (wide) return tile(fmt, size, mt, ic<2>{}, ic<8>{});
-            if (a.n <= 256 * 16) return tile(fmt, size, mt, ic<1>{}, ic<decltype(mt)::value <= 16 ? 16 : 8>{});
+            if (a.n <= 256 * 16) return tile(fmt, size, mt, ic<1>{}, ic<16>{});
             return tile(fmt, size, mt, ic<1>{}, ic<8>{});
         };
-        return a.m == 1 ? rows(ic<1>{}) : a.m <= FEW ? rows(ic<FEW>{}) : a.m <= 16 ? rows(ic<16>{}) : rows(ic<32>{});
+        return a.m == 1 ? rows(ic<1>{}) : a.m <= FEW ? rows(ic<FEW>{}) : rows(ic<16>{});
     };
     if (f == Format::FLOAT) return shape(std::integral_constant<Format, Format::FLOAT>{}, ic<32>{});
     using I = std::integral_constant<Format, Format::INTEGER>;

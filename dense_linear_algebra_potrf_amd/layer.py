@@ -254,12 +254,14 @@ def weight_quant(W, *, format: str = "int4", group: int | None = None, zeros: bo
 
 
 def weight_matvec(x, codes, scales, zeros=None, *, format: str = "int4", group: int | None = None,
-                  x_scales=None, out=None, out_dtype=None, stream=None):
+                  x_scales=None, out=None, out_dtype=None, workspace=None, stream=None):
     """y = x W^T for x [m, k] and 4-bit weights as weight_quant gives them.
 
     x is bfloat16 or float16, or float8_e4m3fn with x_scales as rmsnorm_quant
     gives them (float32 [m], or float8_e8m0fnu [m, ceil(k / 32)]).  y [m, n] is
     `out`, or a new tensor of out_dtype (x's type, bfloat16 for 8-bit x).
+    workspace: a uint8 tensor of weight_matvec_workspace(m, k) bytes (0 up to 16
+    rows), allocated by the call where it is None.
     """
     lib = _lib or _bind()
     xt = _TYPES.get(x.dtype, -1)
@@ -295,9 +297,29 @@ def weight_matvec(x, codes, scales, zeros=None, *, format: str = "int4", group: 
         out = torch.empty((*x.shape[:-1], n), dtype=out_dtype, device=x.device)
     yt = _float_type(out, "out")
     ldy = _rows(out, "out", out_dtype, (m, n))[2]
-    s = _place(at, (codes, scales, zeros, x_scales, out), stream)
+    wp = None
+    size = 0
+    if workspace is not None:
+        size = workspace.numel()
+        wp = _vector(workspace, "workspace", torch.uint8, size)
+    elif m > 16:
+        size = weight_matvec_workspace(m, k)
+        workspace = torch.empty(size, dtype=torch.uint8, device=x.device)
+        wp = workspace.data_ptr()
+    s = _place(at, (codes, scales, zeros, x_scales, out, workspace), stream)
     st = lib.batchlas_weight_matvec(xt, xs, yt, _FORMATS[format], group, m, n, k, x.data_ptr(), ldx, xp, ldxs,
-                                    codes.data_ptr(), ldc, scales.data_ptr(), lds, zp, ldz, out.data_ptr(), ldy, s)
+                                    codes.data_ptr(), ldc, scales.data_ptr(), lds, zp, ldz, out.data_ptr(), ldy, wp, size, s)
     if st:
         _check(st)
     return out
+
+
+def weight_matvec_workspace(m: int, k: int) -> int:
+    """Bytes of workspace that weight_matvec of this size needs (host-only)."""
+    import ctypes
+    lib = _lib or _bind()
+    size = ctypes.c_int64()
+    st = lib.batchlas_weight_matvec_workspace(m, k, ctypes.byref(size))
+    if st:
+        _check(st)
+    return size.value

@@ -320,10 +320,17 @@ batchlas_status batchlas_weight_quant(batchlas_type type, batchlas_format format
 /*
  * weight_matvec: y = x W^T, y (m x n), x (m x k), W (n x k) held as codes, sums
  * in 32 bits.  Made for the few rows of a decoding step (m up to about 64);
- * any m up to 2^21 is computed, reading W once per 64 rows.
+ * any m up to 2^21 is computed, reading W once per 64 rows.  Where a sum of
+ * codes times x leaves the range of 32 bits, the element is computed again in
+ * 64 bits, so that y is finite, infinite or NaN as the definition has it.
  *   xtype, xscale   F16 or BF16 with NONE, or E4M3 with ROW (xscales float[m])
  *            or BLOCK (bytes, row stride ldxs >= (k + 31) / 32)
  *   ytype    F32, F16 or BF16
+ *   workspace  device memory of at least the bytes that
+ *            batchlas_weight_matvec_workspace gives, aligned to 16 bytes; not
+ *            used (may be NULL) where that is 0, which it is for m <= 16
+ * NOT_SUPPORTED: m beyond 2^21, n beyond 2^24, ldx or ldc beyond 2^27, m * k
+ * beyond 2^34.
  */
 batchlas_status batchlas_weight_matvec(batchlas_type xtype, batchlas_scale xscale,
                                        batchlas_type ytype, batchlas_format format, int64_t group,
@@ -331,7 +338,11 @@ batchlas_status batchlas_weight_matvec(batchlas_type xtype, batchlas_scale xscal
                                        int64_t ldx, const void *xscales, int64_t ldxs,
                                        const uint8_t *codes, int64_t ldc, const void *scales,
                                        int64_t lds, const uint8_t *zeros, int64_t ldz, void *y,
-                                       int64_t ldy, batchlas_stream_t stream);
+                                       int64_t ldy, void *workspace, int64_t workspace_bytes,
+                                       batchlas_stream_t stream);
+
+/* Host-only: the workspace that weight_matvec of this size needs, in bytes. */
+batchlas_status batchlas_weight_matvec_workspace(int64_t m, int64_t k, int64_t *bytes);
 
 /* Static text for a status code. */
 const char *batchlas_status_string(batchlas_status s);

@@ -109,7 +109,7 @@ def test_weight_quant_refusals(lib, over, status, msg):
 
 
 MV = dict(xtype=3, xscale=2, ytype=2, format=0, group=32, m=2, n=4, k=100, x=P, ldx=100, xscales=P, ldxs=4, codes=P,
-          ldc=64, scales=P, lds=4, zeros=P, ldz=4, y=P, ldy=4, stream=None)
+          ldc=64, scales=P, lds=4, zeros=P, ldz=4, y=P, ldy=4, workspace=P, bytes=1 << 30, stream=None)
 
 
 @pytest.mark.parametrize("over,status,msg", [
@@ -122,7 +122,10 @@ MV = dict(xtype=3, xscale=2, ytype=2, format=0, group=32, m=2, n=4, k=100, x=P, 
     (dict(codes=None), 2, "codes is NULL"), (dict(scales=None), 2, "scales is NULL"), (dict(y=None), 2, "y is NULL"),
     (dict(codes=P + 4), 1, "aligned to 16"), (dict(y=P + 1), 1, "not aligned"),
     (dict(xscale=1, xscales=P + 2), 1, "not aligned"), (dict(m=(1 << 21) + 1), 3, "m is beyond"),
-    (dict(n=(1 << 24) + 1, ldy=1 << 25), 3, "n is beyond"), (dict(m=0, x=None, y=None, codes=None), 0, ""),
+    (dict(n=(1 << 24) + 1, ldy=1 << 25), 3, "n is beyond"), (dict(ldx=(1 << 27) + 1), 3, "ldx or ldc is beyond"),
+    (dict(m=1 << 20, k=1 << 20, ldx=1 << 20, ldxs=1 << 15, ldc=1 << 19, lds=1 << 15, ldz=1 << 15), 3, "m * k is beyond"),
+    (dict(m=17, workspace=None), 2, "workspace is NULL"), (dict(m=17, bytes=4095), 1, "workspace_bytes"),
+    (dict(workspace=P + 8), 1, "workspace must be"), (dict(m=0, x=None, y=None, codes=None), 0, ""),
 ])
 def test_weight_matvec_refusals(lib, over, status, msg):
     if over.get("ldc") == 49:
@@ -130,6 +133,16 @@ def test_weight_matvec_refusals(lib, over, status, msg):
     st, text = call(lib, "weight_matvec", MV, list(MV), over)
     assert st == status
     assert msg in text
+
+
+def test_weight_matvec_workspace(lib):
+    size = ctypes.c_int64(-1)
+    for m, k, want in ((0, 1, 0), (16, 5000, 0), (17, 1, 2 * 4096), (64, 8192, 64 * 8192 * 2), (33, 129, 3 * 2 * 4096)):
+        assert lib.batchlas_weight_matvec_workspace(m, k, ctypes.byref(size)) == 0 and size.value == want
+    assert lib.batchlas_weight_matvec_workspace(-1, 5, ctypes.byref(size)) == 1
+    assert lib.batchlas_weight_matvec_workspace(1, 0, ctypes.byref(size)) == 1
+    assert lib.batchlas_weight_matvec_workspace(1 << 22, 5, ctypes.byref(size)) == 3
+    assert lib.batchlas_weight_matvec_workspace(1, 1, None) == 2
 
 
 def test_binding_refuses_host_tensors_and_wrong_types(lib):
