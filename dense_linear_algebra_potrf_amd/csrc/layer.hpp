@@ -62,8 +62,12 @@ struct MatvecArgs {
     const uint8_t* zeros; int64_t ldz;   // may be null
     void* y; int64_t ldy;
 };
-constexpr int64_t kFewRows = 16;         // above it x is laid out anew in the workspace first
-int64_t weight_matvec_workspace(int64_t m, int64_t k);    // bytes
+constexpr int64_t kFewRows = 16;         // above it x is laid out anew in the workspace first:
+// 16-bit floats of whole tiles of 16 rows and 128 columns, then a scale for each row
+inline int64_t packed_bytes(int64_t m, int64_t k) { return (m + 15) / 16 * ((k + 127) / 128) * 4096; }
+inline int64_t weight_matvec_workspace(int64_t m, int64_t k) {
+    return m <= kFewRows ? 0 : packed_bytes(m, k) + (m + 15) / 16 * 64;
+}
 hipError_t weight_matvec(Type xt, Scale xs, Type yt, Format f, int group, const MatvecArgs& a, void* workspace,
                          hipStream_t s);
 

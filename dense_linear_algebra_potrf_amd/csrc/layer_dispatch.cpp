@@ -57,40 +57,28 @@ BL_DECLARE_MATVEC(f8block)
 BL_DECLARE_MATVEC(f8row)
 #undef BL_DECLARE_MATVEC
 
-#define BL_DECLARE_PACK(suf) hipError_t weight_pack_##suf(Format f, const MatvecArgs& a, void* packed, hipStream_t s);
-BL_DECLARE_PACK(bf16)
-BL_DECLARE_PACK(f16)
-BL_DECLARE_PACK(f8block)
-BL_DECLARE_PACK(f8row)
-#undef BL_DECLARE_PACK
-#define BL_DECLARE_MANY(suf)                                                                          \
-    hipError_t weight_many_##suf(bool eight, Type yt, Format f, int group, const MatvecArgs& a,       \
-                                 const void* packed, hipStream_t s);
-BL_DECLARE_MANY(bf16)
-BL_DECLARE_MANY(f16)
+#define BL_DECLARE_MANY(suf)                                                                           \
+    hipError_t weight_many_##suf(Type xt, Scale xs, Type yt, const MatvecArgs& a, void* workspace, hipStream_t s);
+BL_DECLARE_MANY(int32)
+BL_DECLARE_MANY(int64)
+BL_DECLARE_MANY(int128)
+BL_DECLARE_MANY(fp4)
 #undef BL_DECLARE_MANY
-
-int64_t weight_matvec_workspace(int64_t m, int64_t k) {
-    // 16-bit floats of whole tiles of 16 rows and 128 columns
-    return m <= kFewRows ? 0 : (m + 15) / 16 * ((k + 127) / 128) * 4096;
-}
+hipError_t weight_pack(Type xt, Scale xs, Format f, const MatvecArgs& a, void* workspace, hipStream_t s);
 
 hipError_t weight_matvec(Type xt, Scale xs, Type yt, Format f, int group, const MatvecArgs& a, void* workspace,
                          hipStream_t s) {
-    const bool block = xs == Scale::BLOCK;
     if (a.m <= kFewRows) {
         if (xt == Type::BF16) return weight_matvec_bf16(yt, f, group, a, s);
         if (xt == Type::F16) return weight_matvec_f16(yt, f, group, a, s);
-        return block ? weight_matvec_f8block(yt, f, group, a, s) : weight_matvec_f8row(yt, f, group, a, s);
+        return xs == Scale::BLOCK ? weight_matvec_f8block(yt, f, group, a, s) : weight_matvec_f8row(yt, f, group, a, s);
     }
-    const hipError_t e = xt == Type::BF16  ? weight_pack_bf16(f, a, workspace, s)
-                         : xt == Type::F16 ? weight_pack_f16(f, a, workspace, s)
-                         : block           ? weight_pack_f8block(f, a, workspace, s)
-                                           : weight_pack_f8row(f, a, workspace, s);
+    const hipError_t e = weight_pack(xt, xs, f, a, workspace, s);
     if (e != hipSuccess) return e;
-    const bool eight = xt == Type::E4M3;
-    return xt == Type::BF16 || (eight && block) ? weight_many_bf16(eight, yt, f, group, a, workspace, s)
-                                                : weight_many_f16(eight, yt, f, group, a, workspace, s);
+    if (f == Format::FLOAT) return weight_many_fp4(xt, xs, yt, a, workspace, s);
+    return group == 32   ? weight_many_int32(xt, xs, yt, a, workspace, s)
+           : group == 64 ? weight_many_int64(xt, xs, yt, a, workspace, s)
+                         : weight_many_int128(xt, xs, yt, a, workspace, s);
 }
 
 }  // namespace bl

@@ -1,13 +1,20 @@
 // Products of more than 16 rows with 4-bit weights.
 //
 // As weight_matvec_impl.hpp, with up to 64 rows of x to a workgroup, so that the
-// codes are read and unpacked once for them.  What bounds it then is x: every
-// workgroup reads all of it, and in the layout of the matrix cores (16 bytes of
-// each of 16 rows) a load makes 64 requests to the cache.  So x is laid out once
-// before, in the caller's workspace, as the matrix cores take it: 1 KB for each
-// 16 rows and 32 columns, 16 bytes to a lane, in 16-bit floats (8-bit values with
-// their blocks' scale), the columns in the order in which integer codes come
-// apart, rows and columns past the end zero.
+// codes are read and unpacked once for them.  Every workgroup reads all of x, and
+// in the layout of the matrix cores (16 bytes of each of 16 rows) a load makes 64
+// requests to the cache.  So x is laid out once before, in the caller's workspace,
+// as the matrix cores take it: 1 KB for each 16 rows and 32 columns, 16 bytes to a
+// lane, the columns in the order in which integer codes come apart, rows and
+// columns past the end zero.
+//
+// On that occasion x becomes half precision, so that the zero point can be
+// subtracted from the codes (packed, exact) and the sums need no correction:
+// bfloat16 and e4m3 values with block scales, times a power of two per row that
+// brings the row's largest below 2^15.  That is exact for everything down to 2^-29
+// of the row's largest (their 8 and 4 significant bits fit in 11) and off by at
+// most 2^-40 of it below, far under the rounding of the 32-bit sums; the power is
+// taken off the results.
 #pragma once
 
 #include "weight_matvec_impl.hpp"
@@ -15,59 +22,113 @@
 namespace bl {
 namespace weight_matvec_detail {
 
-constexpr int kManyWaves = 8;
+using f16x2 = f16 __attribute__((ext_vector_type(2)));
 
-inline int64_t packed_bytes(int64_t m, int64_t k) {
-    return (m + 15) / 16 * ((k + kChunk - 1) / kChunk) * 4096;
+constexpr int kPackThreads = 512;
+
+// Eight bytes at p, of which `left` belong to the row; the others are zero.
+__device__ __forceinline__ uint64_t load_octet(const uint8_t* p, int left) {
+    uint64_t e = 0;
+    if (left >= 8) {
+        __builtin_memcpy(&e, p, 8);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 7; ++j)
+            if (j < left) e |= uint64_t(p[j]) << (8 * j);
+    }
+    return e;
 }
 
-// One thread for 8 columns of a row.
-template <X XT, bool MIXED>
-__global__ __launch_bounds__(256) void pack_kernel(MatvecArgs a, u32x4* out) {
-    const int64_t octets = (a.k + kChunk - 1) / kChunk * 16, rows = (a.m + 15) / 16 * 16;
-    const int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x;
-    if (id >= rows * octets) return;
-    const int64_t row = id / octets, k = (id - row * octets) * 8;
-    const int left = row < a.m ? int(a.k - k < 8 ? a.k - k : 8) : 0;   // columns that there are
-    u32x4 v = {0, 0, 0, 0};
-    if constexpr (is_eight(XT)) {
-        const uint8_t* p = static_cast<const uint8_t*>(a.x) + row * a.ldx + k;
-        uint64_t e = 0;
-        if (left >= 8) {
-            __builtin_memcpy(&e, p, 8);
-        } else {
+// The largest finite magnitude of 8 columns of x from k on, as bits, without a
+// row's scale.
+template <X XT>
+__device__ __forceinline__ uint32_t top_of(const MatvecArgs& a, int64_t row, int64_t k) {
+    const int left = int(a.k - k < 8 ? a.k - k : 8);
+    uint32_t top = 0;
+    if constexpr (XT == X::BF16) {
+        const Raw8<bf16> v = load8(static_cast<const bf16*>(a.x) + row * a.ldx + k, left);
 #pragma unroll
-            for (int j = 0; j < 7; ++j)
-                if (j < left) e |= uint64_t(p[j]) << (8 * j);
-        }
-        float scale = 1;
-        if (XT == X::F8_BLOCK && left > 0)
-            scale = power_of(static_cast<const uint8_t*>(a.xscales)[row * a.ldxs + k / kScaleBlock]);
-        const Frag f = from_e4m3<in_half(XT)>(uint32_t(e), uint32_t(e >> 32), scale);
-        v = u32x4{f.word[0], f.word[1], f.word[2], f.word[3]};
+        for (int j = 0; j < 8; ++j) top = Max{}(top, magnitude(v[j]) < kInfBits ? magnitude(v[j]) : 0);
     } else {
-        const uint16_t* p = static_cast<const uint16_t*>(a.x) + row * a.ldx + k;
+        const uint64_t e = load_octet(static_cast<const uint8_t*>(a.x) + row * a.ldx + k, left);
+        const float block = power_of(static_cast<const uint8_t*>(a.xscales)[row * a.ldxs + k / kScaleBlock]);
+        static_for<0, 8>([&](auto i) {
+            constexpr int J = decltype(i)::value;
+            const uint32_t m = magnitude(__builtin_amdgcn_cvt_f32_fp8(int(uint32_t(e >> (32 * (J / 4)))), J % 4) * block);
+            top = Max{}(top, m < kInfBits ? m : 0);
+        });
+    }
+    return top;
+}
+
+// Eight columns from k on, as halves, times factor; those from a.k on are zero.
+template <X XT>
+__device__ __forceinline__ u32x4 halves_of(const MatvecArgs& a, int64_t row, int64_t k, float factor) {
+    const int left = int(a.k - k < 8 ? a.k - k : 8);
+    f16x8 h = {0, 0, 0, 0, 0, 0, 0, 0};
+    if constexpr (XT == X::F16) {
+        const f16* p = static_cast<const f16*>(a.x) + row * a.ldx + k;
         if (left >= 8) {
-            __builtin_memcpy(&v, p, 16);
+            __builtin_memcpy(&h, p, 16);
         } else {
 #pragma unroll
-            for (int j = 0; j < 7; ++j)
-                if (j < left) v[j / 2] |= uint32_t(p[j]) << (16 * (j & 1));
+            for (int j = 0; j < 7; ++j) h[j] = j < left ? p[j] : f16(0);
+        }
+    } else if constexpr (XT == X::BF16) {
+        const Raw8<bf16> v = load8(static_cast<const bf16*>(a.x) + row * a.ldx + k, left);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[j] = f16(v[j] * factor);
+    } else {
+        const uint64_t e = load_octet(static_cast<const uint8_t*>(a.x) + row * a.ldx + k, left);
+        // 8 columns lie in one block; its scale and the row's factor one after the other,
+        // their product may leave the range
+        const float block = XT == X::F8_BLOCK ? power_of(static_cast<const uint8_t*>(a.xscales)[row * a.ldxs + k / kScaleBlock]) : 1.0f;
+        static_for<0, 8>([&](auto i) {
+            constexpr int J = decltype(i)::value;
+            const float v = __builtin_amdgcn_cvt_f32_fp8(int(uint32_t(e >> (32 * (J / 4)))), J % 4);
+            h[J] = f16(XT == X::F8_BLOCK ? v * block * factor : v);
+        });
+    }
+    return __builtin_bit_cast(u32x4, h);
+}
+
+// A workgroup for a row of x (of whole tiles of 16): its largest finite magnitude,
+// then 8 columns a thread at a time.
+template <X XT, bool MIXED>
+__global__ __launch_bounds__(kPackThreads) void pack_kernel(MatvecArgs a, u32x4* out, float* row_scale) {
+    __shared__ uint32_t tops[kPackThreads / 64];
+    const int64_t row = blockIdx.x, octets = (a.k + kChunk - 1) / kChunk * 16;
+    const bool real = row < a.m;
+    float factor = 1, scale = 1;
+    if (XT == X::F8_ROW && real) scale = static_cast<const float*>(a.xscales)[row];
+    if constexpr (XT == X::BF16 || XT == X::F8_BLOCK) {
+        uint32_t top = 0;
+        for (int64_t k = threadIdx.x * 8; real && k < a.k; k += kPackThreads * 8) top = Max{}(top, top_of<XT>(a, row, k));
+        top = block_reduce<kPackThreads / 64>(top, Max{}, tops);
+        if (top) {
+            const int e = int(top >> 23), up = 141 - e < 126 ? 141 - e : 126;   // largest: 2^14 to 2^15
+            factor = __builtin_bit_cast(float, uint32_t(127 + up) << 23);
+            scale = up < 126 ? __builtin_bit_cast(float, uint32_t(127 - up) << 23) : 0x1p-126f;
         }
     }
-    if constexpr (MIXED) v = mixed<false>(v);
-    // (16 rows, 32 columns), then the lane: row, and which 8 of the columns
-    out[((row / 16) * (octets / 4) + k / 32) * 64 + k % 32 / 8 * 16 + row % 16] = v;
+    if (threadIdx.x == 0 && real) row_scale[row] = scale;
+    for (int64_t o = threadIdx.x; o < octets; o += kPackThreads) {
+        u32x4 v = {0, 0, 0, 0};
+        if (real && o * 8 < a.k) v = halves_of<XT>(a, row, o * 8, factor);
+        if constexpr (MIXED) v = mixed<false>(v);
+        // (16 rows, 32 columns), then the lane: row, and which 8 of the columns
+        out[(row / 16 * (octets / 4) + o / 4) * 64 + o % 4 * 16 + row % 16] = v;
+    }
 }
 
-template <bool HALF, Format F, int GROUP, int MT, int NB>
-__global__ __launch_bounds__(64 * kManyWaves) void weight_many_kernel(MatvecArgs a, const u32x4* packed, X xt, Type yt) {
-    constexpr bool OFFSET = F == Format::INTEGER;
+template <Format F, int GROUP, int MT, int NB, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void weight_many_kernel(MatvecArgs a, const u32x4* packed, const float* row_scale,
+                                                                     X xt, Type yt) {
     constexpr int MB = MT / 16, GROUPS = kChunk / GROUP, STEPS = GROUP / 32, TILE = 16 * NB;
     __shared__ uint32_t scales[kGroups][TILE];
     __shared__ union {
-        u32x4 codes[kManyWaves][NB * 64];
-        float sums[kManyWaves][MB * NB * 4][64];
+        u32x4 codes[WAVES][NB * 64];
+        float sums[WAVES][MB * NB * 4][64];
     } lds;
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -135,32 +196,30 @@ __global__ __launch_bounds__(64 * kManyWaves) void weight_many_kernel(MatvecArgs
             wave_lds_sync();
 #pragma unroll
             for (int s = 0; s < GROUPS; ++s) {
-                f32x4 part[MB][NB], ones[MB];
-                float scale[NB], zero[NB];
+                f32x4 part[MB][NB];
+                float scale[NB];
+                f16x2 zero[NB];
 #pragma unroll
                 for (int j = 0; j < NB; ++j) {
                     const uint32_t v = scales[group + s][16 * j + r];
                     scale[j] = __builtin_bit_cast(float, F == Format::FLOAT ? v : v & 0xffff0000u);
-                    zero[j] = float(v & 0xffu);
-                }
+                    const f16 z = f16(float(v & 0xffu));
+                    zero[j] = f16x2{z, z};
 #pragma unroll
-                for (int i = 0; i < MB; ++i) {
-                    ones[i] = f32x4{0, 0, 0, 0};
-#pragma unroll
-                    for (int j = 0; j < NB; ++j) part[i][j] = f32x4{0, 0, 0, 0};
+                    for (int i = 0; i < MB; ++i) part[i][j] = f32x4{0, 0, 0, 0};
                 }
 #pragma unroll
                 for (int q = 0; q < STEPS; ++q) {
                     const int t = s * STEPS + q;
-                    if constexpr (OFFSET) {
-#pragma unroll
-                        for (int i = 0; i < MB; ++i) ones[i] = product<HALF>(x[i][t], ones_of<HALF>(), ones[i]);
-                    }
 #pragma unroll
                     for (int j = 0; j < NB; ++j) {
-                        const Frag w = unpack<HALF, F, true>(get_codes(j, t));
+                        Frag w = unpack<true, F, true>(get_codes(j, t));
+                        if constexpr (F == Format::INTEGER) {
 #pragma unroll
-                        for (int i = 0; i < MB; ++i) part[i][j] = product<HALF>(x[i][t], w, part[i][j]);
+                            for (uint32_t& v : w.word) v = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, v) - zero[j]);
+                        }
+#pragma unroll
+                        for (int i = 0; i < MB; ++i) part[i][j] = product<true>(x[i][t], w, part[i][j]);
                     }
                     // x of the next chunk (of this one again, at the end), in the place of what has
                     // been multiplied; not earlier, or it would be held twice
@@ -172,10 +231,7 @@ __global__ __launch_bounds__(64 * kManyWaves) void weight_many_kernel(MatvecArgs
 #pragma unroll
                     for (int i = 0; i < MB; ++i)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float p = OFFSET ? fmadd(-zero[j], ones[i][e], part[i][j][e]) : part[i][j][e];
-                            acc[i][j][e] = fmadd(scale[j], p, acc[i][j][e]);
-                        }
+                        for (int e = 0; e < 4; ++e) acc[i][j][e] = fmadd(scale[j], part[i][j][e], acc[i][j][e]);
             }
         }
     }
@@ -188,35 +244,39 @@ __global__ __launch_bounds__(64 * kManyWaves) void weight_many_kernel(MatvecArgs
 #pragma unroll
             for (int e = 0; e < 4; ++e) lds.sums[wave][(i * NB + j) * 4 + e][lane] = acc[i][j][e];
     __syncthreads();
-    store_sums<F, GROUP, MB, NB>(a, xt, yt, m0, n0, rows_m, rows_n, waves, &lds.sums[0]);
+    store_sums<F, GROUP, MB, NB>(a, xt, yt, m0, n0, rows_m, rows_n, waves, &lds.sums[0], row_scale);
 }
 
-template <bool HALF>
-inline hipError_t weight_many_t(X xt, Type yt, Format f, int group, const MatvecArgs& a, const u32x4* packed, hipStream_t s) {
+// x's layout in the workspace: the tiles, then the rows' scales.
+inline float* row_scales(const MatvecArgs& a, void* workspace) {
+    return reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + packed_bytes(a.m, a.k));
+}
+
+template <Format F, int GROUP>
+inline hipError_t weight_many_t(X xt, Type yt, const MatvecArgs& a, void* workspace, hipStream_t s) {
     const int64_t chunks = (a.k + kChunk - 1) / kChunk;
-    const dim3 block(uint32_t(64 * (chunks < kManyWaves ? chunks : kManyWaves)));
-    auto tile = [&](auto fmt, auto size, auto mt, auto nb) {
-        constexpr int MT = decltype(mt)::value, NB = decltype(nb)::value;
+    auto tile = [&](auto mt, auto nb, auto waves) {
+        constexpr int MT = decltype(mt)::value, NB = decltype(nb)::value, WAVES = decltype(waves)::value;
+        const dim3 block(uint32_t(64 * (chunks < WAVES ? chunks : WAVES)));
         const dim3 grid(uint32_t((a.n + 16 * NB - 1) / (16 * NB)), uint32_t((a.m + MT - 1) / MT));
-        return launch(weight_many_kernel<HALF, decltype(fmt)::value, decltype(size)::value, MT, NB>, grid, block, 0, s, a, packed,
-                      xt, yt);
+        return launch(weight_many_kernel<F, GROUP, MT, NB, WAVES>, grid, block, 0, s, a, static_cast<const u32x4*>(workspace),
+                      static_cast<const float*>(row_scales(a, workspace)), xt, yt);
     };
-    auto shape = [&](auto fmt, auto size) {
-        const bool wide = a.n >= 256 * 32;                      // enough rows for every compute unit at 32 each
-        if (a.m <= 32) return wide ? tile(fmt, size, ic<32>{}, ic<2>{}) : tile(fmt, size, ic<32>{}, ic<1>{});
-        return wide ? tile(fmt, size, ic<64>{}, ic<2>{}) : tile(fmt, size, ic<64>{}, ic<1>{});
+    // 32 rows of W to a workgroup where that leaves one for every compute unit
+    auto rows = [&](auto mt) {
+        if (a.n >= 256 * 32) return tile(mt, ic<2>{}, ic<8>{});
+        return tile(mt, ic<1>{}, ic<8>{});
     };
-    if (f == Format::FLOAT) return shape(std::integral_constant<Format, Format::FLOAT>{}, ic<32>{});
-    using I = std::integral_constant<Format, Format::INTEGER>;
-    return group == 32 ? shape(I{}, ic<32>{}) : group == 64 ? shape(I{}, ic<64>{}) : shape(I{}, ic<128>{});
+    return a.m <= 32 ? rows(ic<32>{}) : rows(ic<64>{});
 }
 
 template <X XT>
-inline hipError_t pack_t(Format f, const MatvecArgs& a, u32x4* packed, hipStream_t s) {
-    const int64_t threads = (a.m + 15) / 16 * 16 * ((a.k + kChunk - 1) / kChunk) * 16;
-    const dim3 grid(uint32_t((threads + 255) / 256));
-    return f == Format::INTEGER ? launch(pack_kernel<XT, true>, grid, dim3(256), 0, s, a, packed)
-                                : launch(pack_kernel<XT, false>, grid, dim3(256), 0, s, a, packed);
+inline hipError_t pack_t(Format f, const MatvecArgs& a, void* workspace, hipStream_t s) {
+    const dim3 grid(uint32_t((a.m + 15) / 16 * 16));
+    u32x4* out = static_cast<u32x4*>(workspace);
+    float* scales = row_scales(a, workspace);
+    return f == Format::INTEGER ? launch(pack_kernel<XT, true>, grid, dim3(kPackThreads), 0, s, a, out, scales)
+                                : launch(pack_kernel<XT, false>, grid, dim3(kPackThreads), 0, s, a, out, scales);
 }
 
 }  // namespace weight_matvec_detail

@@ -40,6 +40,9 @@ using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
 enum class X : int { BF16, F16, F8_BLOCK, F8_ROW };
 constexpr bool in_half(X x) { return x == X::F16 || x == X::F8_ROW; }
 constexpr bool is_eight(X x) { return x == X::F8_BLOCK || x == X::F8_ROW; }
+inline X kind_of(Type xt, Scale xs) {
+    return xt == Type::BF16 ? X::BF16 : xt == Type::F16 ? X::F16 : xs == Scale::BLOCK ? X::F8_BLOCK : X::F8_ROW;
+}
 
 constexpr int kChunk = 128;       // columns a wavefront takes at a time
 constexpr int kGroups = 256;      // groups of a row whose scales are in LDS at a time
@@ -209,10 +212,11 @@ __device__ __forceinline__ void stage_scales(const MatvecArgs& a, int64_t n0, in
     }
 }
 
-// Joins the wavefronts' sums (slot of four rows by lane) and stores the tile's y.
+// Joins the wavefronts' sums (slot of four rows by lane), times the scale of x's
+// row if there is one, and stores the tile's y.
 template <Format F, int GROUP, int MB, int NB>
 __device__ __forceinline__ void store_sums(const MatvecArgs& a, X xt, Type yt, int64_t m0, int64_t n0, int rows_m, int rows_n,
-                                           int waves, const float (*sums)[MB * NB * 4][64]) {
+                                           int waves, const float (*sums)[MB * NB * 4][64], const float* row_scale) {
     constexpr int TILE = 16 * NB;
     const int lane = threadIdx.x & 63;
     // whole wavefronts: the detour below takes all lanes
@@ -224,7 +228,7 @@ __device__ __forceinline__ void store_sums(const MatvecArgs& a, X xt, Type yt, i
         float v = 0;
         if (in) {
             for (int w = 0; w < waves; ++w) v += sums[w][slot][from];
-            if (xt == X::F8_ROW) v *= static_cast<const float*>(a.xscales)[m];
+            if (row_scale) v *= row_scale[m];
         }
         for (uint64_t odd = __ballot(magnitude(v) >= kInfBits); odd; odd &= odd - 1) {
             const int at = __builtin_ctzll(odd);
@@ -451,7 +455,8 @@ __global__ __launch_bounds__(64 * WAVES) void weight_matvec_kernel(MatvecArgs a,
             for (int e = 0; e < SUMS; ++e) lds.sums[wave][(i * NB + j) * 4 + e][lane] = acc[i][j][e];
     __syncthreads();
 
-    store_sums<F, GROUP, MB, NB>(a, XT, yt, m0, n0, rows_m, rows_n, waves, &lds.sums[0]);
+    store_sums<F, GROUP, MB, NB>(a, XT, yt, m0, n0, rows_m, rows_n, waves, &lds.sums[0],
+                                XT == X::F8_ROW ? static_cast<const float*>(a.xscales) : nullptr);
 }
 
 template <X XT>

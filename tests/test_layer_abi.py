@@ -137,7 +137,9 @@ def test_weight_matvec_refusals(lib, over, status, msg):
 
 def test_weight_matvec_workspace(lib):
     size = ctypes.c_int64(-1)
-    for m, k, want in ((0, 1, 0), (16, 5000, 0), (17, 1, 2 * 4096), (64, 8192, 64 * 8192 * 2), (33, 129, 3 * 2 * 4096)):
+    # halves of whole tiles of 16 rows and 128 columns, and a float for each row
+    for m, k, want in ((0, 1, 0), (16, 5000, 0), (17, 1, 2 * 4096 + 128), (64, 8192, 64 * 8192 * 2 + 256),
+                       (33, 129, 3 * 2 * 4096 + 192)):
         assert lib.batchlas_weight_matvec_workspace(m, k, ctypes.byref(size)) == 0 and size.value == want
     assert lib.batchlas_weight_matvec_workspace(-1, 5, ctypes.byref(size)) == 1
     assert lib.batchlas_weight_matvec_workspace(1, 0, ctypes.byref(size)) == 1
