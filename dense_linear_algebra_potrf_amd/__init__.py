@@ -229,7 +229,8 @@ def version() -> int:
 # ---------------------------------------------------------------- low-bit layer operators
 # In modules of their own, which import torch; loaded at first use.
 _LAZY = {"rmsnorm_quant": "layer", "rmsnorm_grad": "layer", "rmsnorm_grad_workspace": "layer",
-         "weight_quant": "layer", "weight_matvec": "layer", "weight_matvec_workspace": "layer"}
+         "weight_quant": "layer", "weight_matvec": "layer", "weight_matvec_workspace": "layer",
+         "calibrate_weights": "calibrate", "second_moments": "calibrate"}
 
 
 def __getattr__(name: str):
