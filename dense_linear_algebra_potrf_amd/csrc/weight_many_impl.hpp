@@ -125,7 +125,7 @@ template <Format F, int GROUP, int MT, int NB, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void weight_many_kernel(MatvecArgs a, const u32x4* packed, const float* row_scale,
                                                                      X xt, Type yt) {
     constexpr int MB = MT / 16, GROUPS = kChunk / GROUP, STEPS = GROUP / 32, TILE = 16 * NB;
-    __shared__ uint32_t scales[kGroups][TILE];
+    __shared__ Scales<F, GROUPS, TILE> scales;
     __shared__ union {
         u32x4 codes[WAVES][NB * 64];
         float sums[WAVES][MB * NB * 4][64];
@@ -185,7 +185,7 @@ __global__ __launch_bounds__(64 * WAVES) void weight_many_kernel(MatvecArgs a, c
         }
         const int g0 = base * GROUPS;
         if (base) __syncthreads();
-        stage_scales<F, GROUPS, TILE>(a, n0, g0, end * GROUPS < groups ? end * GROUPS - g0 : groups - g0, scales);
+        scales.stage(a, n0, g0, end * GROUPS < groups ? end * GROUPS - g0 : groups - g0);
         __syncthreads();
         for (; c < end; c += waves) {
             const int next = c + waves < end ? c + waves : c, group = (c - base) * GROUPS;
@@ -194,16 +194,16 @@ __global__ __launch_bounds__(64 * WAVES) void weight_many_kernel(MatvecArgs a, c
             for (int i = 0; i < NB; ++i) own[64 * i + (lane & ~3) + ((lane & 3) ^ (lane >> 4))] = held[i];
             load_codes(next, held);
             wave_lds_sync();
+            float scale[NB][GROUPS], zeros[NB][GROUPS];
+#pragma unroll
+            for (int j = 0; j < NB; ++j) scales.get(16 * j + r, group, scale[j], zeros[j]);
 #pragma unroll
             for (int s = 0; s < GROUPS; ++s) {
                 f32x4 part[MB][NB];
-                float scale[NB];
                 f16x2 zero[NB];
 #pragma unroll
                 for (int j = 0; j < NB; ++j) {
-                    const uint32_t v = scales[group + s][16 * j + r];
-                    scale[j] = __builtin_bit_cast(float, F == Format::FLOAT ? v : v & 0xffff0000u);
-                    const f16 z = f16(float(v & 0xffu));
+                    const f16 z = f16(zeros[j][s]);
                     zero[j] = f16x2{z, z};
 #pragma unroll
                     for (int i = 0; i < MB; ++i) part[i][j] = f32x4{0, 0, 0, 0};
@@ -231,7 +231,7 @@ __global__ __launch_bounds__(64 * WAVES) void weight_many_kernel(MatvecArgs a, c
 #pragma unroll
                     for (int i = 0; i < MB; ++i)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[i][j][e] = fmadd(scale[j], part[i][j][e], acc[i][j][e]);
+                        for (int e = 0; e < 4; ++e) acc[i][j][e] = fmadd(scale[j][s], part[i][j][e], acc[i][j][e]);
             }
         }
     }

@@ -177,40 +177,68 @@ __device__ __forceinline__ double by_definition(const MatvecArgs& a, X xt, Forma
     return sum;
 }
 
-// Scales of `count` groups from `first` on, of the TILE rows of W from n0 on, to
-// LDS: a float's bits (FLOAT), or its upper half with the zero point in the lower.
-// Neighbouring lanes take neighbouring rows and 8 groups each, so that the writes
-// spread over the banks.  Groups that the last chunk lacks (a chunk has GROUPS)
-// get a finite scale; their products are zero.
+// Scales and zero points of kGroups groups of TILE rows of W, in LDS as they lie
+// in memory; rows are padded so that 16 of them spread over the banks.  A chunk
+// has GROUPS groups.
 template <Format F, int GROUPS, int TILE>
-__device__ __forceinline__ void stage_scales(const MatvecArgs& a, int64_t n0, int first, int count, uint32_t (*scales)[TILE]) {
-    constexpr int SB = F == Format::FLOAT ? 1 : 2;              // bytes of a scale
-    const int rounded = (count + GROUPS - 1) / GROUPS * GROUPS;
-    for (int e = threadIdx.x; e < (rounded + 7) / 8 * TILE; e += blockDim.x) {
-        const int row = e % TILE, at = e / TILE * 8, left = count - at;
-        const int64_t n = n0 + row < a.n ? n0 + row : a.n - 1;
-        const uint8_t* p = static_cast<const uint8_t*>(a.scales) + (n * a.lds + first + at) * SB;
-        const uint8_t* q = a.zeros + n * a.ldz + first + at;
-        if (left >= 8) {
-            uint8_t s[8 * SB], z[8] = {8, 8, 8, 8, 8, 8, 8, 8};
-            __builtin_memcpy(s, p, sizeof(s));
-            if (SB == 2 && a.zeros) __builtin_memcpy(z, q, 8);
+struct Scales {
+    static constexpr int SB = F == Format::FLOAT ? 1 : 2;       // bytes of a scale
+    alignas(8) uint8_t scale[TILE][kGroups * SB + 4 * SB];
+    alignas(4) uint8_t zero[F == Format::FLOAT ? 1 : TILE][kGroups + 4];
+
+    // `count` groups from `first` on, of the rows from n0 on.  Groups that the last
+    // chunk lacks get zeros; their products are zero.
+    __device__ __forceinline__ void stage(const MatvecArgs& a, int64_t n0, int first, int count) {
+        const int octets = ((count + GROUPS - 1) / GROUPS * GROUPS + 7) / 8;
+        for (int e = threadIdx.x; e < octets * TILE; e += blockDim.x) {
+            const int row = e / octets, at = e % octets * 8, left = count - at;
+            const int64_t n = n0 + row < a.n ? n0 + row : a.n - 1;
+            const uint8_t* p = static_cast<const uint8_t*>(a.scales) + (n * a.lds + first + at) * SB;
+            const uint8_t* q = a.zeros + n * a.ldz + first + at;
+            uint8_t s[8 * SB] = {};
+            uint64_t z = 0x0808080808080808u;
+            if (left >= 8) {
+                __builtin_memcpy(s, p, 8 * SB);
+                if (SB == 2 && a.zeros) __builtin_memcpy(&z, q, 8);
+            } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                scales[at + j][row] = SB == 1 ? __builtin_bit_cast(uint32_t, power_of(s[j]))
-                                              : uint32_t(s[j * SB + SB - 1]) << 24 | uint32_t(s[j * SB]) << 16 | z[j];
-        } else {
-#pragma unroll 1
-            for (int j = 0; j < 8 && at + j < rounded; ++j) {
-                uint32_t v = 0;
-                if (j < left)
-                    v = SB == 1 ? __builtin_bit_cast(uint32_t, power_of(p[j]))
-                                : uint32_t(p[j * SB + SB - 1]) << 24 | uint32_t(p[j * SB]) << 16 | (a.zeros ? q[j] : 8);
-                scales[at + j][row] = v;
+                for (int j = 0; j < 7; ++j)
+                    if (j < left) {
+#pragma unroll
+                        for (int i = 0; i < SB; ++i) s[j * SB + i] = p[j * SB + i];
+                        if (SB == 2 && a.zeros) z = (z & ~(0xffull << (8 * j))) | uint64_t(q[j]) << (8 * j);
+                    }
+            }
+            // the padding takes what a row's last octet has over
+#pragma unroll
+            for (int i = 0; i < SB; ++i) __builtin_memcpy(&scale[row][at * SB + 8 * i], s + 8 * i, 8);
+            if constexpr (SB == 2) {
+                __builtin_memcpy(&zero[row][at], &z, 4);
+                __builtin_memcpy(&zero[row][at + 4], reinterpret_cast<const uint8_t*>(&z) + 4, 4);
             }
         }
     }
-}
+
+    // Those of a row's groups from `group` on, a multiple of GROUPS.
+    __device__ __forceinline__ void get(int row, int group, float (&s)[GROUPS], float (&z)[GROUPS]) const {
+        uint64_t v = 0;
+        __builtin_memcpy(&v, __builtin_assume_aligned(&scale[row][group * SB], GROUPS * SB), GROUPS * SB);
+        uint32_t w = 0;
+        if constexpr (SB == 2) __builtin_memcpy(&w, __builtin_assume_aligned(&zero[row][group], GROUPS), GROUPS);
+#pragma unroll
+        for (int i = 0; i < GROUPS; ++i) {
+            if constexpr (SB == 2) {
+                const uint32_t half = uint32_t(v >> (32 * (i / 2)));
+                s[i] = __builtin_bit_cast(float, i & 1 ? half & 0xffff0000u : half << 16);
+                z[i] = float(w >> (8 * i) & 255u);
+            } else {
+                // 2^128, infinity, for a byte of 255: the sum is then not finite, and NaN by the definition
+                s[i] = __builtin_amdgcn_ldexpf(1.0f, int(uint32_t(v) >> (8 * i) & 255u) - 127);
+                z[i] = 0;
+            }
+        }
+    }
+};
 
 // Joins the wavefronts' sums (slot of four rows by lane), times the scale of x's
 // row if there is one, and stores the tile's y.
@@ -257,7 +285,7 @@ __global__ __launch_bounds__(64 * WAVES) void weight_matvec_kernel(MatvecArgs a,
     // or the codes on their way out of it, whichever is less
     constexpr bool MIXED = F == Format::INTEGER && 4 * H::PIECES <= 8 * NB;
     constexpr int SUMS = MT < 4 ? MT : 4;                       // of a lane's four sums, those of rows of x
-    __shared__ uint32_t scales[kGroups][TILE];                  // of the groups at hand
+    __shared__ Scales<F, GROUPS, TILE> scales;                  // of the groups at hand
     __shared__ union {
         struct { u32x4 codes[NB * 64]; u32x4 x[MT * SLOTS]; } of[WAVES];
         float sums[WAVES][MB * NB * 4][64];
@@ -383,16 +411,12 @@ __global__ __launch_bounds__(64 * WAVES) void weight_matvec_kernel(MatvecArgs a,
         for (int i = 0; i < MB; ++i) xscale[i] = XT == X::F8_BLOCK ? d.xscale[i] : 0;
         if (next < full) load(next, d);
         wave_lds_sync();
+        float scale[NB][GROUPS], zero[NB][GROUPS];
+#pragma unroll
+        for (int j = 0; j < NB; ++j) scales.get(16 * j + r, group, scale[j], zero[j]);
 #pragma unroll
         for (int s = 0; s < GROUPS; ++s) {
             f32x4 part[MB][NB], ones[MB];
-            float scale[NB], zero[NB];
-#pragma unroll
-            for (int j = 0; j < NB; ++j) {
-                const uint32_t v = scales[group + s][16 * j + r];
-                scale[j] = __builtin_bit_cast(float, F == Format::FLOAT ? v : v & 0xffff0000u);
-                zero[j] = float(v & 0xffu);
-            }
 #pragma unroll
             for (int i = 0; i < MB; ++i) {
                 ones[i] = f32x4{0, 0, 0, 0};
@@ -422,8 +446,8 @@ __global__ __launch_bounds__(64 * WAVES) void weight_matvec_kernel(MatvecArgs a,
                 for (int i = 0; i < MB; ++i)
 #pragma unroll
                     for (int e = 0; e < SUMS; ++e) {
-                        const float p = OFFSET ? fmadd(-zero[j], ones[i][e], part[i][j][e]) : part[i][j][e];
-                        acc[i][j][e] = fmadd(scale[j], p, acc[i][j][e]);
+                        const float p = OFFSET ? fmadd(-zero[j][s], ones[i][e], part[i][j][e]) : part[i][j][e];
+                        acc[i][j][e] = fmadd(scale[j][s], p, acc[i][j][e]);
                     }
             }
         }
@@ -438,7 +462,7 @@ __global__ __launch_bounds__(64 * WAVES) void weight_matvec_kernel(MatvecArgs a,
         if (c < full) load(c, held);                            // on its way while the scales are staged
         const int g0 = base * GROUPS;
         if (base) __syncthreads();
-        stage_scales<F, GROUPS, TILE>(a, n0, g0, end * GROUPS < groups ? end * GROUPS - g0 : groups - g0, scales);
+        scales.stage(a, n0, g0, end * GROUPS < groups ? end * GROUPS - g0 : groups - g0);
         __syncthreads();
         for (; c < end; c += waves) {
             if (c >= whole) load_partial(held);
