@@ -24,8 +24,6 @@ namespace weight_matvec_detail {
 
 using f16x2 = f16 __attribute__((ext_vector_type(2)));
 
-constexpr int kPackThreads = 512;
-
 // Eight bytes at p, of which `left` belong to the row; the others are zero.
 __device__ __forceinline__ uint64_t load_octet(const uint8_t* p, int left) {
     uint64_t e = 0;
@@ -39,85 +37,96 @@ __device__ __forceinline__ uint64_t load_octet(const uint8_t* p, int left) {
     return e;
 }
 
-// The largest finite magnitude of 8 columns of x from k on, as bits, without a
-// row's scale.
+// Eight columns of a row of x; those past its end are zero.
 template <X XT>
-__device__ __forceinline__ uint32_t top_of(const MatvecArgs& a, int64_t row, int64_t k) {
-    const int left = int(a.k - k < 8 ? a.k - k : 8);
-    uint32_t top = 0;
-    if constexpr (XT == X::BF16) {
-        const Raw8<bf16> v = load8(static_cast<const bf16*>(a.x) + row * a.ldx + k, left);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) top = Max{}(top, magnitude(v[j]) < kInfBits ? magnitude(v[j]) : 0);
-    } else {
-        const uint64_t e = load_octet(static_cast<const uint8_t*>(a.x) + row * a.ldx + k, left);
-        const float block = power_of(static_cast<const uint8_t*>(a.xscales)[row * a.ldxs + k / kScaleBlock]);
-        static_for<0, 8>([&](auto i) {
-            constexpr int J = decltype(i)::value;
-            const uint32_t m = magnitude(__builtin_amdgcn_cvt_f32_fp8(int(uint32_t(e >> (32 * (J / 4)))), J % 4) * block);
-            top = Max{}(top, m < kInfBits ? m : 0);
-        });
-    }
-    return top;
-}
+struct Octet {
+    using T = std::conditional_t<XT == X::F16, f16, bf16>;
+    std::conditional_t<is_eight(XT), uint64_t, Raw8<T>> raw;
+    float block;                                                // the scale of the block they lie in
 
-// Eight columns from k on, as halves, times factor; those from a.k on are zero.
-template <X XT>
-__device__ __forceinline__ u32x4 halves_of(const MatvecArgs& a, int64_t row, int64_t k, float factor) {
-    const int left = int(a.k - k < 8 ? a.k - k : 8);
-    f16x8 h = {0, 0, 0, 0, 0, 0, 0, 0};
-    if constexpr (XT == X::F16) {
-        const f16* p = static_cast<const f16*>(a.x) + row * a.ldx + k;
-        if (left >= 8) {
-            __builtin_memcpy(&h, p, 16);
+    __device__ __forceinline__ void load(const MatvecArgs& a, int64_t row, int64_t k) {
+        const int left = int(a.k - k < 8 ? a.k - k : 8);
+        if constexpr (is_eight(XT)) {
+            raw = load_octet(static_cast<const uint8_t*>(a.x) + row * a.ldx + k, left);
+            block = XT == X::F8_BLOCK ? power_of(static_cast<const uint8_t*>(a.xscales)[row * a.ldxs + k / kScaleBlock]) : 1.0f;
         } else {
-#pragma unroll
-            for (int j = 0; j < 7; ++j) h[j] = j < left ? p[j] : f16(0);
+            raw = load8(static_cast<const T*>(a.x) + row * a.ldx + k, left);
         }
-    } else if constexpr (XT == X::BF16) {
-        const Raw8<bf16> v = load8(static_cast<const bf16*>(a.x) + row * a.ldx + k, left);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) h[j] = f16(v[j] * factor);
-    } else {
-        const uint64_t e = load_octet(static_cast<const uint8_t*>(a.x) + row * a.ldx + k, left);
-        // 8 columns lie in one block; its scale and the row's factor one after the other,
-        // their product may leave the range
-        const float block = XT == X::F8_BLOCK ? power_of(static_cast<const uint8_t*>(a.xscales)[row * a.ldxs + k / kScaleBlock]) : 1.0f;
-        static_for<0, 8>([&](auto i) {
-            constexpr int J = decltype(i)::value;
-            const float v = __builtin_amdgcn_cvt_f32_fp8(int(uint32_t(e >> (32 * (J / 4)))), J % 4);
-            h[J] = f16(XT == X::F8_BLOCK ? v * block * factor : v);
-        });
     }
-    return __builtin_bit_cast(u32x4, h);
-}
+    template <int J>
+    __device__ __forceinline__ float get() const {
+        if constexpr (is_eight(XT)) return __builtin_amdgcn_cvt_f32_fp8(int(uint32_t(raw >> (32 * (J / 4)))), J % 4) * block;
+        else return raw[J];
+    }
+    // The largest finite magnitude, as bits.
+    __device__ __forceinline__ uint32_t top() const {
+        uint32_t most = 0;
+        static_for<0, 8>([&](auto i) {
+            const uint32_t m = magnitude(get<decltype(i)::value>());
+            most = Max{}(most, m < kInfBits ? m : 0);
+        });
+        return most;
+    }
+    // As halves, times the row's factor.
+    __device__ __forceinline__ u32x4 halves(float factor) const {
+        if constexpr (XT == X::F16) return __builtin_bit_cast(u32x4, raw);
+        f16x8 h;
+        static_for<0, 8>([&](auto i) { h[decltype(i)::value] = f16(get<decltype(i)::value>() * factor); });
+        return __builtin_bit_cast(u32x4, h);
+    }
+};
 
 // A workgroup for a row of x (of whole tiles of 16): its largest finite magnitude,
-// then 8 columns a thread at a time.
+// then 8 columns a thread at a time; the first kKept of them stay in registers.
+constexpr int kPackThreads = 512, kKept = 4;
+
 template <X XT, bool MIXED>
 __global__ __launch_bounds__(kPackThreads) void pack_kernel(MatvecArgs a, u32x4* out, float* row_scale) {
     __shared__ uint32_t tops[kPackThreads / 64];
     const int64_t row = blockIdx.x, octets = (a.k + kChunk - 1) / kChunk * 16;
-    const bool real = row < a.m;
+    const int64_t mine = row < a.m ? (a.k + 7) / 8 : 0;         // octets that hold columns
+    auto put = [&](int64_t o, u32x4 v) {
+        if constexpr (MIXED) v = mixed<false>(v);
+        // (16 rows, 32 columns), then the lane: row, and which 8 of the columns
+        out[(row / 16 * (octets / 4) + o / 4) * 64 + o % 4 * 16 + row % 16] = v;
+    };
+    Octet<XT> kept[kKept];
+#pragma unroll
+    for (int i = 0; i < kKept; ++i)
+        if (threadIdx.x + i * kPackThreads < mine) kept[i].load(a, row, (threadIdx.x + i * kPackThreads) * 8);
     float factor = 1, scale = 1;
-    if (XT == X::F8_ROW && real) scale = static_cast<const float*>(a.xscales)[row];
+    if (XT == X::F8_ROW && row < a.m) scale = static_cast<const float*>(a.xscales)[row];
     if constexpr (XT == X::BF16 || XT == X::F8_BLOCK) {
         uint32_t top = 0;
-        for (int64_t k = threadIdx.x * 8; real && k < a.k; k += kPackThreads * 8) top = Max{}(top, top_of<XT>(a, row, k));
+#pragma unroll
+        for (int i = 0; i < kKept; ++i)
+            if (threadIdx.x + i * kPackThreads < mine) top = Max{}(top, kept[i].top());
+        for (int64_t o = threadIdx.x + kKept * kPackThreads; o < mine; o += kPackThreads) {
+            Octet<XT> v;
+            v.load(a, row, o * 8);
+            top = Max{}(top, v.top());
+        }
         top = block_reduce<kPackThreads / 64>(top, Max{}, tops);
         if (top) {
             const int e = int(top >> 23), up = 141 - e < 126 ? 141 - e : 126;   // largest: 2^14 to 2^15
             factor = __builtin_bit_cast(float, uint32_t(127 + up) << 23);
-            scale = up < 126 ? __builtin_bit_cast(float, uint32_t(127 - up) << 23) : 0x1p-126f;
+            scale = __builtin_bit_cast(float, uint32_t(127 - up) << 23);
         }
     }
-    if (threadIdx.x == 0 && real) row_scale[row] = scale;
-    for (int64_t o = threadIdx.x; o < octets; o += kPackThreads) {
-        u32x4 v = {0, 0, 0, 0};
-        if (real && o * 8 < a.k) v = halves_of<XT>(a, row, o * 8, factor);
-        if constexpr (MIXED) v = mixed<false>(v);
-        // (16 rows, 32 columns), then the lane: row, and which 8 of the columns
-        out[(row / 16 * (octets / 4) + o / 4) * 64 + o % 4 * 16 + row % 16] = v;
+    if (threadIdx.x == 0 && row < a.m) row_scale[row] = scale;
+#pragma unroll
+    for (int i = 0; i < kKept; ++i) {
+        const int64_t o = threadIdx.x + i * kPackThreads;
+        if (o < octets) put(o, o < mine ? kept[i].halves(factor) : u32x4{0, 0, 0, 0});
+    }
+    for (int64_t o = threadIdx.x + kKept * kPackThreads; o < octets; o += kPackThreads) {
+        u32x4 h = {0, 0, 0, 0};
+        if (o < mine) {
+            Octet<XT> v;
+            v.load(a, row, o * 8);
+            h = v.halves(factor);
+        }
+        put(o, h);
     }
 }
 

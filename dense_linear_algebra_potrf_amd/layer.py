@@ -7,6 +7,9 @@ allocates belong to the current stream.
 """
 from __future__ import annotations
 
+import ctypes
+import functools
+
 import torch
 
 _TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2, torch.float8_e4m3fn: 3}
@@ -96,7 +99,7 @@ def rmsnorm_quant(x, weight, residual=None, *, eps: float = 1e-6, scale: str = "
     ty = _float_type(x, "x")
     at = _gpu(x)
     rows, n, ldx = _rows(x, "x")
-    dt, dev = x.dtype, x.device
+    dt = x.dtype
     w = _vector(weight, "weight", dt, n)
     if scale not in _SCALES:
         raise ValueError('scale must be "block" or "row"')
@@ -105,23 +108,23 @@ def rmsnorm_quant(x, weight, residual=None, *, eps: float = 1e-6, scale: str = "
     if residual is not None:
         ldr = _rows(residual, "residual", dt, (rows, n))[2]
         if residual_out is None:
-            residual_out = torch.empty(x.shape, dtype=dt, device=dev)
+            residual_out = torch.empty_like(x)
         ldh = _rows(residual_out, "residual_out", dt, (rows, n))[2]
         rp, hp = residual.data_ptr(), residual_out.data_ptr()
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
     if out is None:
-        out = torch.empty(x.shape, dtype=_E4M3, device=dev)
+        out = torch.empty_like(x, dtype=_E4M3)
     ldq = _rows(out, "out", _E4M3, (rows, n))[2]
     lds = 0
     if scale == "block":
         blocks = (n + 31) // 32
         if scales is None:
-            scales = torch.empty((rows, blocks), dtype=_E8M0, device=dev)
+            scales = x.new_empty((rows, blocks), dtype=_E8M0)
         lds = _rows(scales, "scales", _E8M0, (rows, blocks))[2]
     else:
         if scales is None:
-            scales = torch.empty(rows, dtype=torch.float32, device=dev)
+            scales = x.new_empty(rows, dtype=torch.float32)
         _vector(scales, "scales", torch.float32, rows)
     s = _place(at, (weight, residual, residual_out, out, scales), stream)
     st = lib.batchlas_rmsnorm_quant(ty, _SCALES[scale], rows, n, x.data_ptr(), ldx, rp, ldr, w, eps,
@@ -145,22 +148,22 @@ def rmsnorm_grad(dy, h, weight, dh=None, *, eps: float = 1e-6, dx=None, dweight=
     ty = _float_type(h, "h")
     at = _gpu(h)
     rows, n, ldh = _rows(h, "h")
-    dt, dev = h.dtype, h.device
+    dt = h.dtype
     lddy = _rows(dy, "dy", dt, (rows, n))[2]
     w = _vector(weight, "weight", dt, n)
     lddh = _rows(dh, "dh", dt, (rows, n))[2] if dh is not None else 0
     if dx is None:
-        dx = torch.empty(h.shape, dtype=dt, device=dev)
+        dx = torch.empty_like(h)
     lddx = _rows(dx, "dx", dt, (rows, n))[2]
     wp = dp = None
     size = 0
     if dweight is not False:
         if dweight is None:
-            dweight = torch.empty(n, dtype=torch.float32, device=dev)
+            dweight = h.new_empty(n, dtype=torch.float32)
         dp = _vector(dweight, "dweight", torch.float32, n)
         if workspace is None:
             size = rmsnorm_grad_workspace(h.dtype, rows, n)
-            workspace = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
+            workspace = h.new_empty(size, dtype=torch.uint8) if size else None
         if workspace is not None:
             size = workspace.numel()
             wp = _vector(workspace, "workspace", torch.uint8, size)
@@ -173,9 +176,9 @@ def rmsnorm_grad(dy, h, weight, dh=None, *, eps: float = 1e-6, dx=None, dweight=
     return dx, (dweight if dp else None)
 
 
+@functools.lru_cache(maxsize=1024)
 def rmsnorm_grad_workspace(dtype, rows: int, n: int) -> int:
     """Bytes of workspace that rmsnorm_grad of this size needs (host-only)."""
-    import ctypes
     lib = _lib or _bind()
     size = ctypes.c_int64()
     st = lib.batchlas_rmsnorm_grad_workspace(_TYPES.get(dtype, -1), rows, n, ctypes.byref(size))
@@ -214,7 +217,6 @@ def weight_quant(W, *, format: str = "int4", group: int | None = None, zeros: bo
     ty = _float_type(W, "W")
     at = _gpu(W)
     n, k, ldw = _rows(W, "W")
-    dev = W.device
     st_type = _scale_type(format)
     if group is None:
         group = 128 if format == "int4" else 32
@@ -222,24 +224,24 @@ def weight_quant(W, *, format: str = "int4", group: int | None = None, zeros: bo
         raise ValueError("group must be positive")
     groups = -(-k // group)
     if codes is None:
-        codes = torch.empty((n, (k + 31) // 32 * 16), dtype=torch.uint8, device=dev)
+        codes = W.new_empty((n, (k + 31) // 32 * 16), dtype=torch.uint8)
     if codes.shape[0] != n:
         raise ValueError(f"codes must have {n} rows")
     ldc = _codes(codes, k)[1]
     if scales is None:
-        scales = torch.empty((n, groups), dtype=st_type, device=dev)
+        scales = W.new_empty((n, groups), dtype=st_type)
     lds = _rows(scales, "scales", st_type, (n, groups))[2]
     zp = vp = None
     ldz = ldv = 0
     if zeros:
         if zeros_out is None:
-            zeros_out = torch.empty((n, groups), dtype=torch.uint8, device=dev)
+            zeros_out = W.new_empty((n, groups), dtype=torch.uint8)
         ldz = _rows(zeros_out, "zeros_out", torch.uint8, (n, groups))[2]
         zp = zeros_out.data_ptr()
     elif zeros_out is not None:
         raise ValueError("zeros_out needs zeros=True")
     if values is True:
-        values = torch.empty(W.shape, dtype=W.dtype, device=dev)
+        values = torch.empty_like(W)
     elif values is False:
         values = None
     if values is not None:
@@ -294,7 +296,7 @@ def weight_matvec(x, codes, scales, zeros=None, *, format: str = "int4", group: 
         raise ValueError("x_scales is for 8-bit x")
     if out is None:
         out_dtype = out_dtype or (torch.bfloat16 if xt == 3 else x.dtype)
-        out = torch.empty((*x.shape[:-1], n), dtype=out_dtype, device=x.device)
+        out = x.new_empty((*x.shape[:-1], n), dtype=out_dtype)
     yt = _float_type(out, "out")
     ldy = _rows(out, "out", out_dtype, (m, n))[2]
     wp = None
@@ -304,7 +306,7 @@ def weight_matvec(x, codes, scales, zeros=None, *, format: str = "int4", group: 
         wp = _vector(workspace, "workspace", torch.uint8, size)
     elif m > 16:
         size = weight_matvec_workspace(m, k)
-        workspace = torch.empty(size, dtype=torch.uint8, device=x.device)
+        workspace = x.new_empty(size, dtype=torch.uint8)
         wp = workspace.data_ptr()
     s = _place(at, (codes, scales, zeros, x_scales, out, workspace), stream)
     st = lib.batchlas_weight_matvec(xt, xs, yt, _FORMATS[format], group, m, n, k, x.data_ptr(), ldx, xp, ldxs,
@@ -314,9 +316,9 @@ def weight_matvec(x, codes, scales, zeros=None, *, format: str = "int4", group: 
     return out
 
 
+@functools.lru_cache(maxsize=1024)
 def weight_matvec_workspace(m: int, k: int) -> int:
     """Bytes of workspace that weight_matvec of this size needs (host-only)."""
-    import ctypes
     lib = _lib or _bind()
     size = ctypes.c_int64()
     st = lib.batchlas_weight_matvec_workspace(m, k, ctypes.byref(size))

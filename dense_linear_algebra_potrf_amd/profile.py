@@ -17,6 +17,9 @@ kernel family and the workload) holding the commands, the per-kernel statistics
 and the counter table, and a `<workload>.counters.json` with the calibrated
 HBM traffic per launch that bench.py attaches to its roofline while the
 family's sources are unchanged.
+
+`python -m dense_linear_algebra_potrf_amd.profile --raw DIR --out DIR --layer` does the same for the listed
+cases of perf/operators.py (the low-bit layer operators), into layer_operators.md.
 """
 from __future__ import annotations
 
@@ -105,7 +108,9 @@ def read_csv(outdir: str, suffix: str) -> list[dict]:
 
 def short_name(name: str) -> str:
     name = name.replace("void ", "").replace("bl::tiny_detail::", "").replace("bl::blocked_detail::", "")
-    name = name.replace("bl::lds_detail::", "").replace("bl::potrs_detail::", "").replace("bl::", "")
+    name = name.replace("bl::lds_detail::", "").replace("bl::potrs_detail::", "")
+    name = name.replace("bl::rmsnorm_detail::", "").replace("bl::weight_quant_detail::", "")
+    name = name.replace("bl::weight_matvec_detail::", "").replace("bl::", "")
     return name.split("(")[0]
 
 
@@ -273,14 +278,98 @@ def summary_md(name, cfg, stats, kern, vals, rec, cmds) -> str:
     return "\n".join(lines)
 
 
+# ---------------------------------------------------------------- the low-bit layer operators
+LAYER_KERNELS = "rmsnorm_|weight_|pack_kernel"
+LAYER_PASSES = [
+    ["FETCH_SIZE"],
+    ["WRITE_SIZE", "GRBM_GUI_ACTIVE"],
+    ["SQ_INSTS_VALU", "SQ_ACTIVE_INST_VALU", "SQ_VALU_MFMA_BUSY_CYCLES", "SQ_LDS_IDX_ACTIVE",
+     "SQ_LDS_BANK_CONFLICT", "SQ_WAIT_INST_ANY", "SQ_WAVE_CYCLES", "SQ_BUSY_CU_CYCLES", "GRBM_GUI_ACTIVE"],
+]
+
+
+def layer_module():
+    import importlib.util
+    spec = importlib.util.spec_from_file_location("operators", os.path.join(ROOT, "perf", "operators.py"))
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    m.own = True
+    return m
+
+
+def run_layer_case(name: str, passes: int) -> None:
+    """The program under the profiler: passes through a listed case, on three sets of inputs in turn."""
+    import torch
+    m = layer_module()
+    case = next(c for c in m.listed() if c["name"] == name)
+    states = [m.prepare(case, seed) for seed in (1, 2, 3)]
+    for i in range(passes):
+        m.run(states[i % 3])
+    torch.cuda.synchronize()
+    print(f"ran {name}", flush=True)
+
+
+def profile_layer(raw: str, outdir: str, ffac: float, wfac: float, calib_cmds: list[str]) -> None:
+    m = layer_module()
+    cmd = lambda name, passes: ["python3", os.path.abspath(__file__), "--run-layer", name, "--passes", str(passes)]  # noqa: E731
+    rows, kernels = [], []
+    for case in m.listed():
+        name, work = case["name"], m.work(case)
+        out = run_rocprof(["--kernel-trace", "--stats"], cmd(name, 60), os.path.join(raw, f"{name}_stats"))
+        mine = [s for s in kernel_stats(out) if any(k in s["name"] for k in LAYER_KERNELS.split("|"))]
+        if not mine:
+            raise RuntimeError(f"no library kernel in the trace of {name}")
+        sums: dict[str, float] = {}
+        for i, group in enumerate(LAYER_PASSES):
+            out = run_rocprof(["--pmc", *group, "--kernel-include-regex", LAYER_KERNELS], cmd(name, 6),
+                              os.path.join(raw, f"{name}_pmc{i}"))
+            for s in mine:
+                for k, v in counters(out, s["name"]).items():
+                    sums[k] = sums.get(k, 0.0) + (v if k != "GRBM_GUI_ACTIVE" or i == 2 else 0.0)
+        us = sum(s["avg_us"] for s in mine)
+        gui = sums["GRBM_GUI_ACTIVE"] / XCDS
+        rows.append(f"| {name} | {us:.2f} | {work['bytes'] / 1e6:.2f} | {work['bytes'] / us / 1e6:.2f} | "
+                    f"{sums['FETCH_SIZE'] * 1024 * ffac / 1e6:.2f} / {sums['WRITE_SIZE'] * 1024 * wfac / 1e6:.2f} | "
+                    f"{100 * 4 * sums['SQ_ACTIVE_INST_VALU'] / (gui * SIMDS):.0f}% | "
+                    f"{100 * sums['SQ_VALU_MFMA_BUSY_CYCLES'] / (gui * SIMDS):.0f}% | "
+                    f"{100 * sums['SQ_LDS_IDX_ACTIVE'] / (gui * CUS):.0f}% | "
+                    f"{100 * sums['SQ_WAIT_INST_ANY'] / sums['SQ_WAVE_CYCLES']:.0f}% |")
+        for s in mine:
+            kernels.append(f"| {name} | `{short_name(s['name'])}` | {s['calls']} | {s['avg_us']:.2f} | {s['min_us']:.2f} | "
+                           f"{s['max_us']:.2f} |")
+        print(f"[profile] {name}: {us:.2f} us", flush=True)
+    lines = ["# rocprofv3: the low-bit layer operators, listed cases of perf/operators.py", "",
+             "Written by `python -m dense_linear_algebra_potrf_amd.profile --raw <raw> --out profiles --layer`, which ran for",
+             "each case, from /tmp with TMPDIR=/tmp on one MI355X (three sets of inputs in turn):", "", "```",
+             "rocprofv3 --kernel-trace --stats --output-format csv -d <out> -o run -- python3 profile.py --run-layer CASE --passes 60",
+             *[f"rocprofv3 --pmc {' '.join(g)} --kernel-include-regex '{LAYER_KERNELS}' --output-format csv -d <out> -o run -- "
+               "python3 profile.py --run-layer CASE --passes 6" for g in LAYER_PASSES], *calib_cmds, "```", "",
+             "A pass's kernels together; TB/s is the case's own bytes (each input read once, each output written once) over",
+             "their time; busy fractions are of the SIMD (VALU, MFMA) and CU (LDS) cycles while the kernels ran, waiting is",
+             "`SQ_WAIT_INST_ANY` over the wave cycles:", "",
+             "| Case | Kernels (µs) | Bytes (MB) | TB/s | HBM read / written (MB) | VALU busy | MFMA busy | LDS busy | Waiting |",
+             "|---|---|---|---|---|---|---|---|---|", *rows, "", "| Case | Kernel | Calls | Average (µs) | Min (µs) | Max (µs) |",
+             "|---|---|---|---|---|---|", *kernels, ""]
+    with open(os.path.join(outdir, "layer_operators.md"), "w") as f:
+        f.write("\n".join(lines))
+
+
 def main(argv=None) -> int:
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
-    ap.add_argument("--raw", required=True, help="directory for rocprofv3's raw output")
-    ap.add_argument("--out", required=True, help="directory for the summaries")
+    ap.add_argument("--layer", action="store_true", help="profile the cases of perf/operators.py instead")
+    ap.add_argument("--run-layer", help=argparse.SUPPRESS)
+    ap.add_argument("--passes", type=int, default=60, help=argparse.SUPPRESS)
+    ap.add_argument("--raw", help="directory for rocprofv3's raw output")
+    ap.add_argument("--out", help="directory for the summaries")
     ap.add_argument("--config", action="append", choices=sorted(bench.CONFIGS))
     ap.add_argument("--reparse", action="store_true",
                     help="rebuild the summaries from the raw output of an earlier run")
     a = ap.parse_args(argv)
+    if a.run_layer:
+        run_layer_case(a.run_layer, a.passes)
+        return 0
+    if not a.raw or not a.out:
+        ap.error("--raw and --out are required")
     global REPARSE
     REPARSE = a.reparse
     a.raw, a.out = os.path.abspath(a.raw), os.path.abspath(a.out)
@@ -288,6 +377,9 @@ def main(argv=None) -> int:
     os.makedirs(a.out, exist_ok=True)
     ffac, wfac, calib_cmds = calibrate(a.raw)
     print(f"[profile] calibration: FETCH_SIZE x{ffac:.3f}, WRITE_SIZE x{wfac:.3f}", flush=True)
+    if a.layer:
+        profile_layer(a.raw, a.out, ffac, wfac, calib_cmds)
+        return 0
     for name in a.config or [bench.PRIMARY] + bench.SECONDARY:
         profile_config(name, a.raw, a.out, ffac, wfac, calib_cmds)
     return 0
