@@ -11,7 +11,7 @@ hipError_t rmsnorm_grad_bf16(const NormGradArgs& a, hipStream_t s) {
     return rmsnorm_detail::rmsnorm_grad_t<layer::bf16>(a, s);
 }
 int64_t rmsnorm_grad_partials_bf16(int64_t rows, int64_t n) {
-    return rmsnorm_detail::grad_partials(rows, n);
+    return rmsnorm_detail::grad_partials<layer::bf16>(rows, n);
 }
 
 }  // namespace bl

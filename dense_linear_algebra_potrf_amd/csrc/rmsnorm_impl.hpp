@@ -1,11 +1,20 @@
 // Root-mean-square norm with the residual's addition and an output in 8 bits,
 // and its gradient.
 //
+//     h = x + r,  s = 1 / sqrt(mean(h^2) + eps),  v = h s w,  q = e4m3(v / scale)
+//
 // A row is read once: it stays in the registers of the TPR threads that share
 // it (VPT vectors of 8 elements each, vector i of thread t at column
 // 8 (i TPR + t)) from the load through the sum of squares to the stores.  A
 // block of 32 columns is then held by 4 neighbouring lanes, so its largest
 // magnitude takes two quad permutes.
+//
+// HBM bounds it: 2 + 2 + 2 + 1 bytes an element in 16 bits with a residual.
+// 8192 x 8192 bf16, residual, block scales: 97 us, 4.9 TB/s where a large copy
+// reaches 5.1.  A single row of 4096 takes 7.3 us a call, of which the kernel
+// is less than the launch.  Loading a row ahead in a grid of 1280 workgroups
+// took 102 us at that size (registers for half as many wavefronts), 3 to 7%
+// less below 1024 columns: not done.
 #pragma once
 
 #include "layer_impl.hpp"
@@ -119,9 +128,18 @@ __global__ __launch_bounds__(Shape<TPR>::threads) void rmsnorm_quant_kernel(Norm
     }
 }
 
-// The gradient.  Each workgroup takes rows blockIdx, blockIdx + grid, ... and
-// keeps its sum of dw in registers over them; the sums of the workgroups go to
-// `partial` and are added in a fixed order by rmsnorm_dw_kernel.
+// The gradient, with g = dy w and the residual's own dh:
+//     dx = s (g - h s^2 mean(g h)) + dh,   dw = sum over rows of dy h s.
+// Each workgroup takes rows blockIdx, blockIdx + grid, ... and keeps its sum of
+// dw in registers over them; the sums of the workgroups go to `partial` and are
+// added in a fixed order by rmsnorm_dw_kernel: no atomics, so two runs agree
+// bit for bit.
+//
+// HBM bounds it (four rows of 16 bits an element in and out with dh).  With
+// only 512 workgroups to hide it, the latency of a row's load showed: 8192 x
+// 4096 bf16 took 80 us, and 52 (5.1 TB/s) with the next row on its way while
+// this one is reduced and stored.  Where two rows and a sum do not fit the
+// registers (more than 8 bytes a column and thread) it loads in order.
 template <typename T, int TPR, int VPT>
 __global__ __launch_bounds__(Shape<TPR>::threads) void rmsnorm_grad_kernel(NormGradArgs a, float* dw) {
     using S = Shape<TPR>;
@@ -239,7 +257,9 @@ __global__ __launch_bounds__(Shape<TPR>::threads) void rmsnorm_grad_kernel(NormG
 }
 
 // dw[c] = the sum of `count` rows of partial sums: 32 columns and 8 slices of
-// the rows per workgroup, the slices joined in LDS.
+// the rows per workgroup, the slices joined in LDS.  Bound by latency: 512 rows
+// of 4096 take 4 us with eight loads of a slice on their way at a time; one at
+// a time cost 517 x 1537 f32 two of its 16 us.
 static __global__ __launch_bounds__(256) void rmsnorm_dw_kernel(const float* partial, int64_t count, int n, float* dw) {
     __shared__ float slice[8][33];
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
@@ -272,7 +292,10 @@ static __global__ __launch_bounds__(256) void rmsnorm_zero_kernel(float* dw, int
 
 // ---------------------------------------------------------------- selection
 // Calls f with the shape that holds a row of n columns: one wavefront up to
-// 1024 columns, then 256 to 1024 threads.
+// 1024 columns (no barrier), then 256 or 512 threads.  Three vectors a thread
+// are there since idle lanes hold registers and do not load: bf16 rows with a
+// residual of 5120, 9001 and 12288 columns (16 M elements) take 30.9, 35.5 and
+// 29.9 us with 3 and 33.2, 43.3 and 33.5 with the next power of two.
 template <typename F>
 inline hipError_t with_shape(int64_t n, F&& f) {
     const int64_t v = (n + 7) / 8;
@@ -280,20 +303,29 @@ inline hipError_t with_shape(int64_t n, F&& f) {
     if (v <= 128) return f(ic<64>{}, ic<2>{});
     if (v <= 256) return f(ic<256>{}, ic<1>{});
     if (v <= 512) return f(ic<256>{}, ic<2>{});
+    if (v <= 768) return f(ic<256>{}, ic<3>{});
     if (v <= 1024) return f(ic<256>{}, ic<4>{});
+    if (v <= 1536) return f(ic<512>{}, ic<3>{});
     if (v <= 2048) return f(ic<512>{}, ic<4>{});
     return f(ic<512>{}, ic<8>{});
 }
 
 // The gradient holds two rows and a sum, so it spreads them over more threads.
-template <typename F>
+// Three vectors in 16 bits: 34.8 us for 3276 x 5120 and 44.4 for 1365 x 12288
+// (47.6 and 56.6 with the next power of two).  In 32 bits three vectors leave
+// no room for the next row, which up to 8192 columns two vectors of 512 threads
+// have: 56.0 us against 58.0 at 5120.
+template <typename T, typename F>
 inline hipError_t with_grad_shape(int64_t n, F&& f) {
     const int64_t v = (n + 7) / 8;
     if (v <= 64) return f(ic<64>{}, ic<1>{});
     if (v <= 128) return f(ic<64>{}, ic<2>{});
     if (v <= 256) return f(ic<256>{}, ic<1>{});
     if (v <= 512) return f(ic<256>{}, ic<2>{});
+    if constexpr (sizeof(T) == 2)
+        if (v <= 768) return f(ic<256>{}, ic<3>{});
     if (v <= 1024) return f(ic<512>{}, ic<2>{});
+    if (v <= 1536) return f(ic<512>{}, ic<3>{});
     return f(ic<512>{}, ic<4>{});
 }
 
@@ -321,9 +353,10 @@ inline int64_t grad_groups(int64_t rows) {
     return need < most ? need : most;
 }
 
+template <typename T>
 inline int64_t grad_partials(int64_t rows, int64_t n) {
     int64_t p = 0;
-    with_grad_shape(n, [&](auto tpr, auto) {
+    with_grad_shape<T>(n, [&](auto tpr, auto) {
         constexpr int TPR = decltype(tpr)::value;
         p = grad_groups<TPR>(rows) * Shape<TPR>::rows;
         return hipSuccess;
@@ -335,9 +368,9 @@ template <typename T>
 inline hipError_t rmsnorm_grad_t(const NormGradArgs& a, hipStream_t s) {
     if (a.rows == 0)
         return launch(rmsnorm_zero_kernel, dim3(uint32_t((a.n + 255) / 256)), dim3(256), 0, s, a.dw, int(a.n));
-    const int64_t parts = grad_partials(a.rows, a.n);
+    const int64_t parts = grad_partials<T>(a.rows, a.n);
     float* out = !a.dw ? nullptr : parts > 1 ? a.partial : a.dw;
-    const hipError_t e = with_grad_shape(a.n, [&](auto tpr, auto vpt) {
+    const hipError_t e = with_grad_shape<T>(a.n, [&](auto tpr, auto vpt) {
         constexpr int TPR = decltype(tpr)::value, VPT = decltype(vpt)::value;
         return launch(rmsnorm_grad_kernel<T, TPR, VPT>, dim3(uint32_t(grad_groups<TPR>(a.rows))),
                       dim3(Shape<TPR>::threads), 0, s, a, out);
