@@ -423,6 +423,87 @@ def test_matvec_exact_integers(kind, fmt, group, zeros):
 
 @pytest.mark.parametrize("kind", ["bf16", "f16", "f8block", "f8row"])
 @pytest.mark.parametrize("fmt,group,zeros", FORMS)
+def test_matvec_many_columns_and_long_rows(kind, fmt, group, zeros):
+    """Exact, as above: n where a workgroup takes 32 rows of W (with a last one that
+    is not full), 16 rows and 8 or 16 wavefronts, at every number of rows of x that
+    has its own kernel; and k where a row has more groups than are held at a time."""
+    import torch
+    import dense_linear_algebra_potrf_amd as bl
+    long = 256 * group                              # columns of the groups held at a time
+    sizes = [(1, 8200, 300), (4, 8193, 129), (8, 8223, 257), (16, 8192, 130), (20, 8201, 200), (40, 8195, 290),
+             (2, 4100, 257), (19, 4097, 140), (1, 33, long + 17), (5, 20, 2 * long + 300), (16, 17, long + 1),
+             (21, 18, long + 33), (64, 33, long + 129)]
+    if fmt == "int4" and group > 32:
+        sizes = sizes[:2] + sizes[5:6] + sizes[8:]
+    for i, (m, n, k) in enumerate(sizes):
+        announce("weight_matvec wide", kind, fmt, group, zeros, m, n, k)
+        codes, sc, z, cuda = make_weights(i, n, k, fmt, group, zeros, exact=True)
+        x64, x, xs = make_x(i + 40, m, k, kind, exact=True)
+        want = x64 @ ref.held(codes, sc, z, fmt, group, k).T
+        y = bl.weight_matvec(x, *cuda, format=fmt, group=group, x_scales=xs, out_dtype=torch.float32)
+        got = ref.f64(y)
+        assert np.array_equal(got, want), f"{int((got != want).sum())} of {want.size} differ"
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f8block", "f8row"])
+@pytest.mark.parametrize("fmt,group,zeros", [("int4", 32, False), ("int4", 128, True), ("fp4", 32, False)])
+def test_matvec_many_rows_that_are_not_finite(kind, fmt, group, zeros):
+    """More than 16 rows, each with its own range: infinities, NaN, rows of zeros,
+    rows of one value near the type's largest, rows down to its smallest ones."""
+    import torch
+    import dense_linear_algebra_potrf_amd as bl
+    announce("weight_matvec many rows not finite", kind, fmt, group, zeros)
+    m, n, k = 37, 50, 300
+    codes, sc, z, (cc, cs, cz) = make_weights(3, n, k, fmt, group, zeros, exact=True)
+    x64, x, xs = make_x(4, m, k, kind, exact=True)
+    eight = kind.startswith("f8")
+    big = {"bf16": 3e38, "f16": 6e4}.get(kind, 448.0)
+    v = x.float()
+    if not eight:
+        v[1, 7] = float("inf")
+        v[2, 299] = -float("inf")
+        v[17, 200], v[17, 3] = float("inf"), float("inf")
+    v[3, 100] = float("nan")
+    v[4] = 0
+    v[18] = 0
+    v[18, 33] = big
+    v[19] *= 2.0 ** (-126 if kind == "bf16" else -20 if kind == "f16" else -6)
+    v[20, 5] *= 2.0 ** (30 if kind == "bf16" else 8 if kind == "f16" else 3)      # one that dwarfs its row
+    x = v.to(x.dtype)
+    s2 = cs.float()
+    s2[5, 1], sc[5, 1] = float("nan"), np.nan
+    if fmt == "int4":
+        s2[11, 0], sc[11, 0] = float("inf"), np.inf
+    if kind == "f8block":
+        raw_scales = xs.view(torch.uint8)
+        raw_scales[30, 2], raw_scales[31, 1], raw_scales[32], raw_scales[33, 0] = 255, 200, 0, 20
+        b = raw_scales.cpu().numpy()
+        xw = np.repeat(np.where(b == 255, np.nan, 2.0 ** (b.astype(np.float64) - 127)), 32, 1)[:, :k]
+    elif kind == "f8row":
+        xs[30], xs[31], xs[32] = float("nan"), float("inf"), 2.0 ** -126
+        xw = ref.f64(xs)[:, None]
+    else:
+        xw = 1.0
+    with np.errstate(all="ignore"):
+        x64 = ref.f64(x.float()) * xw
+        W = ref.held(codes, sc, z, fmt, group, k)
+        want = np.stack([(ref.f64(x.float())[i] * (xw if np.isscalar(xw) else xw[i]) * W).sum(1) for i in range(m)])
+        want32 = want.astype(np.float32)
+        size = (np.abs(np.where(np.isfinite(x64), x64, 0)) @
+                np.repeat(np.where(np.isfinite(sc), sc, 0), group, 1)[:, :k].T)
+    y = bl.weight_matvec(x, cc, s2.to(cs.dtype), cz, format=fmt, group=group, x_scales=xs, out_dtype=torch.float32)
+    got = y.cpu().numpy()
+    assert np.array_equal(np.isnan(got), np.isnan(want32)), np.argwhere(np.isnan(got) != np.isnan(want32))[:8]
+    inf = np.isinf(want32)
+    assert np.array_equal(got[inf], want32[inf])
+    ok = np.isfinite(want32)
+    off = np.abs(got - want)
+    bound = PRODUCT * size + 4 * U * np.abs(want) + SUBNORMAL["f32"]
+    assert (off <= bound)[ok].all(), np.argwhere(ok & ~(off <= bound))[:8]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f8block", "f8row"])
+@pytest.mark.parametrize("fmt,group,zeros", FORMS)
 def test_matvec_error(kind, fmt, group, zeros):
     import torch
     import dense_linear_algebra_potrf_amd as bl
