@@ -96,15 +96,21 @@ __device__ __forceinline__ T row_reduce(T v, F&& f) {
     return v;
 }
 
-template <typename T, typename F>
+// The same over LANES = 16, 32 or 64 neighbouring lanes.
+template <int LANES, typename T, typename F>
 __device__ __forceinline__ T wave_reduce(T v, F&& f) {
     v = row_reduce<16>(v, f);
-    uint32_t u = __builtin_bit_cast(uint32_t, v);
-    auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-    v = f(__builtin_bit_cast(T, uint32_t(a[0])), __builtin_bit_cast(T, uint32_t(a[1])));
-    u = __builtin_bit_cast(uint32_t, v);
-    auto b = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-    return f(__builtin_bit_cast(T, uint32_t(b[0])), __builtin_bit_cast(T, uint32_t(b[1])));
+    if constexpr (LANES >= 32) {
+        const uint32_t u = __builtin_bit_cast(uint32_t, v);
+        auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+        v = f(__builtin_bit_cast(T, uint32_t(a[0])), __builtin_bit_cast(T, uint32_t(a[1])));
+    }
+    if constexpr (LANES >= 64) {
+        const uint32_t u = __builtin_bit_cast(uint32_t, v);
+        auto b = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+        v = f(__builtin_bit_cast(T, uint32_t(b[0])), __builtin_bit_cast(T, uint32_t(b[1])));
+    }
+    return v;
 }
 
 struct Add { __device__ __forceinline__ float operator()(float a, float b) const { return a + b; } };
@@ -112,17 +118,18 @@ struct Max {   // on the bits of magnitudes: a NaN is the largest
     __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const { return a > b ? a : b; }
 };
 
-// The same over the WAVES wavefronts of a workgroup; `slot` is this reduction's
-// own LDS (WAVES entries), so that one barrier is enough.
-template <int WAVES, typename T, typename F>
+// The same over THREADS threads: part of a wavefront, one, or all of a workgroup.
+// `slot` is this reduction's own LDS (an entry per wavefront), so that one barrier
+// is enough.
+template <int THREADS, typename T, typename F>
 __device__ __forceinline__ T block_reduce(T v, F&& f, T* slot) {
-    v = wave_reduce(v, f);
-    if constexpr (WAVES > 1) {
+    v = wave_reduce<(THREADS < 64 ? THREADS : 64)>(v, f);
+    if constexpr (THREADS > 64) {
         if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
         __syncthreads();
         v = slot[0];
 #pragma unroll
-        for (int i = 1; i < WAVES; ++i) v = f(v, slot[i]);
+        for (int i = 1; i < THREADS / 64; ++i) v = f(v, slot[i]);
     }
     return v;
 }

@@ -25,9 +25,9 @@ namespace rmsnorm_detail {
 using namespace layer;
 
 template <int TPR> struct Shape {
-    static constexpr int threads = TPR < 256 ? 256 : TPR;     // one wavefront a row: four rows
+    static constexpr int threads = TPR < 256 ? 256 : TPR;     // of several rows, if a row has fewer
     static constexpr int rows = threads / TPR;
-    static constexpr int waves = TPR / 64;
+    static constexpr int waves = TPR < 64 ? 1 : TPR / 64;     // a row's
 };
 
 // Squares leave the range of 32 bits where the row itself does not.  Outside
@@ -35,9 +35,10 @@ template <int TPR> struct Shape {
 // sum is taken again of h times a power of two that brings the largest to about
 // 1.  The branch is the same for all threads of a row.
 __device__ __forceinline__ bool mean_in_range(float mean) { return mean > 0x1p-90f && mean < 0x1p90f; }
-// That power of two; 1 for a row of zeros or one that is not finite.
+// That power of two (a large one for a row of zeros: eps alone may be too small for
+// the root); 1 for a row that is not finite.
 __device__ __forceinline__ float rescale(uint32_t top) {
-    if (top == 0 || top >= kInfBits) return 1.0f;
+    if (top >= kInfBits) return 1.0f;
     const int e = 127 - int(top >> 23);            // -127..127, kept where f and eps f^2 are finite
     return __builtin_bit_cast(float, uint32_t((e < -126 ? -126 : e < 100 ? e : 100) + 127) << 23);
 }
@@ -71,7 +72,7 @@ __global__ __launch_bounds__(Shape<TPR>::threads) void rmsnorm_quant_kernel(Norm
 #pragma unroll
             for (int j = 0; j < 8; ++j) sum = fmadd(v[i][j], v[i][j], sum);
         }
-        sum = block_reduce<S::waves>(sum, Add{}, sums[0]);
+        sum = block_reduce<TPR>(sum, Add{}, sums[0]);
         float mean = sum / float(n) + a.eps;
         if (!mean_in_range(mean)) {
             uint32_t most = 0;
@@ -79,7 +80,7 @@ __global__ __launch_bounds__(Shape<TPR>::threads) void rmsnorm_quant_kernel(Norm
             for (int i = 0; i < VPT; ++i)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) most = Max{}(most, magnitude(v[i][j]));
-            const float f = rescale(block_reduce<S::waves>(most, Max{}, tops[0]));
+            const float f = rescale(block_reduce<TPR>(most, Max{}, tops[0]));
             sum = 0;
 #pragma unroll
             for (int i = 0; i < VPT; ++i)
@@ -88,7 +89,7 @@ __global__ __launch_bounds__(Shape<TPR>::threads) void rmsnorm_quant_kernel(Norm
                     v[i][j] *= f;
                     sum = fmadd(v[i][j], v[i][j], sum);
                 }
-            mean = block_reduce<S::waves>(sum, Add{}, sums[1]) / float(n) + a.eps * f * f;
+            mean = block_reduce<TPR>(sum, Add{}, sums[1]) / float(n) + a.eps * f * f;
         }
         const float rs = __builtin_amdgcn_rsqf(mean);
         uint32_t top = 0;
@@ -113,7 +114,7 @@ __global__ __launch_bounds__(Shape<TPR>::threads) void rmsnorm_quant_kernel(Norm
             }
         }
         if constexpr (!BLOCK) {
-            top = block_reduce<S::waves>(top, Max{}, tops[1]);
+            top = block_reduce<TPR>(top, Max{}, tops[1]);
             const float big = __builtin_bit_cast(float, top);
             const float scale = top >= kInfBits ? __builtin_nanf("") : fmaxf(big / kE4M3Max, kTiny);
             if (t == 0) static_cast<float*>(a.scales)[row] = scale;
@@ -131,9 +132,10 @@ __global__ __launch_bounds__(Shape<TPR>::threads) void rmsnorm_quant_kernel(Norm
 // The gradient, with g = dy w and the residual's own dh:
 //     dx = s (g - h s^2 mean(g h)) + dh,   dw = sum over rows of dy h s.
 // Each workgroup takes rows blockIdx, blockIdx + grid, ... and keeps its sum of
-// dw in registers over them; the sums of the workgroups go to `partial` and are
-// added in a fixed order by rmsnorm_dw_kernel: no atomics, so two runs agree
-// bit for bit.
+// dw in registers over them, joined over its rows in LDS (16384 x 1024 bf16: 30 us,
+// 39 with a sum per row of the workgroup); the sums of the workgroups go to
+// `partial` and are added in a fixed order by rmsnorm_dw_kernel: no atomics, so two
+// runs agree bit for bit.
 //
 // HBM bounds it (four rows of 16 bits an element in and out with dh).  With
 // only 512 workgroups to hide it, the latency of a row's load showed: 8192 x
@@ -197,8 +199,8 @@ __global__ __launch_bounds__(Shape<TPR>::threads) void rmsnorm_grad_kernel(NormG
             hr[i].keep_packed();
             gr[i].keep_packed();
         }
-        square = block_reduce<S::waves>(square, Add{}, sums[0]);
-        dot = block_reduce<S::waves>(dot, Add{}, sums[1]);
+        square = block_reduce<TPR>(square, Add{}, sums[0]);
+        dot = block_reduce<TPR>(dot, Add{}, sums[1]);
         float mean = square / float(n) + a.eps, f = 1;
         if (!mean_in_range(mean)) {
             uint32_t most = 0;
@@ -206,7 +208,7 @@ __global__ __launch_bounds__(Shape<TPR>::threads) void rmsnorm_grad_kernel(NormG
             for (int i = 0; i < VPT; ++i)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) most = Max{}(most, magnitude(hr[i][j]));
-            f = rescale(block_reduce<S::waves>(most, Max{}, tops));
+            f = rescale(block_reduce<TPR>(most, Max{}, tops));
             square = dot = 0;
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
@@ -219,8 +221,8 @@ __global__ __launch_bounds__(Shape<TPR>::threads) void rmsnorm_grad_kernel(NormG
                 }
             }
             if constexpr (S::waves > 1) __syncthreads();   // sums[1] is read by all before it is written again
-            square = block_reduce<S::waves>(square, Add{}, sums[2]);
-            dot = block_reduce<S::waves>(dot, Add{}, sums[1]);
+            square = block_reduce<TPR>(square, Add{}, sums[2]);
+            dot = block_reduce<TPR>(dot, Add{}, sums[1]);
             mean = square / float(n) + a.eps * f * f;
         }
         // with h f and rs = 1 / rms(h f): s = f rs, and h s = (h f) rs
@@ -246,12 +248,26 @@ __global__ __launch_bounds__(Shape<TPR>::threads) void rmsnorm_grad_kernel(NormG
         }
         if constexpr (S::waves > 1) __syncthreads();   // the next row's sums
     }
-    if (dw && (a.rows > 1 || first == 0)) {      // one row: its sum is dw itself
-        float* out = dw + first * n;
+    if (!dw) return;
+    float* out = dw + int64_t(blockIdx.x) * n;
+    if constexpr (S::rows == 1) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int c = 8 * (i * TPR + t);
             store8(out + c, part[i], n - c);
+        }
+    } else {
+        __shared__ float join[S::rows][TPR * VPT * 8];
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) join[threadIdx.x / TPR][8 * (i * TPR + t) + j] = part[i][j];
+        __syncthreads();
+        for (int c = threadIdx.x; c < n; c += S::threads) {
+            float sum = join[0][c];
+#pragma unroll
+            for (int i = 1; i < S::rows; ++i) sum += join[i][c];
+            out[c] = sum;
         }
     }
 }
@@ -291,14 +307,18 @@ static __global__ __launch_bounds__(256) void rmsnorm_zero_kernel(float* dw, int
 }
 
 // ---------------------------------------------------------------- selection
-// Calls f with the shape that holds a row of n columns: one wavefront up to
-// 1024 columns (no barrier), then 256 or 512 threads.  Three vectors a thread
-// are there since idle lanes hold registers and do not load: bf16 rows with a
-// residual of 5120, 9001 and 12288 columns (16 M elements) take 30.9, 35.5 and
-// 29.9 us with 3 and 33.2, 43.3 and 33.5 with the next power of two.
+// Calls f with the shape that holds a row of n columns: up to 1024 a wavefront or
+// a part of it (no barrier), then 256 or 512 threads.  Lanes without columns hold
+// registers and load nothing, hence the steps between.  bf16 with a residual, 16 M
+// elements, in us:
+//     128 columns   16 lanes 28.2, 64 lanes 66.3     256   32 lanes 27.4, 64: 38.4
+//     1024          64 lanes 27.4, 256: 32.6         512   64 lanes 27.4, 256: 51.6
+//     5120, 9001, 12288   3 vectors a thread 30.9, 35.5, 29.9, 4: 33.2, 43.3, 33.5
 template <typename F>
 inline hipError_t with_shape(int64_t n, F&& f) {
     const int64_t v = (n + 7) / 8;
+    if (v <= 16) return f(ic<16>{}, ic<1>{});
+    if (v <= 32) return f(ic<32>{}, ic<1>{});
     if (v <= 64) return f(ic<64>{}, ic<1>{});
     if (v <= 128) return f(ic<64>{}, ic<2>{});
     if (v <= 256) return f(ic<256>{}, ic<1>{});
@@ -310,7 +330,9 @@ inline hipError_t with_shape(int64_t n, F&& f) {
     return f(ic<512>{}, ic<8>{});
 }
 
-// The gradient holds two rows and a sum, so it spreads them over more threads.
+// The gradient holds two rows and a sum, so it spreads them over more threads; for
+// short rows as above (bf16 with dh, 16 M elements: 128 columns 29 us with 16 lanes,
+// 130 with 64; 256 columns 29 with 32, 78 with 64).
 // Three vectors in 16 bits: 34.8 us for 3276 x 5120 and 44.4 for 1365 x 12288
 // (47.6 and 56.6 with the next power of two).  In 32 bits three vectors leave
 // no room for the next row, which up to 8192 columns two vectors of 512 threads
@@ -318,6 +340,8 @@ inline hipError_t with_shape(int64_t n, F&& f) {
 template <typename T, typename F>
 inline hipError_t with_grad_shape(int64_t n, F&& f) {
     const int64_t v = (n + 7) / 8;
+    if (v <= 16) return f(ic<16>{}, ic<1>{});
+    if (v <= 32) return f(ic<32>{}, ic<1>{});
     if (v <= 64) return f(ic<64>{}, ic<1>{});
     if (v <= 128) return f(ic<64>{}, ic<2>{});
     if (v <= 256) return f(ic<256>{}, ic<1>{});
@@ -344,8 +368,9 @@ inline hipError_t rmsnorm_quant_t(Scale sc, const NormQuantArgs& a, hipStream_t 
     });
 }
 
-// Workgroups of the gradient kernel: two a compute unit, and not less than four
-// rows each, whose sums of dw are then fewer.
+// Workgroups of the gradient kernel: two a compute unit (8192 x 4096 bf16 52 us, 60
+// with four), and not less than four rows for each of its groups of threads, whose
+// sums of dw are then fewer (1024 x 4096 bf16 14.9 us, 17.1 with one).
 template <int TPR>
 inline int64_t grad_groups(int64_t rows) {
     const int64_t need = (rows + 4 * Shape<TPR>::rows - 1) / (4 * Shape<TPR>::rows);
@@ -353,15 +378,15 @@ inline int64_t grad_groups(int64_t rows) {
     return need < most ? need : most;
 }
 
+// Partial sums of dw, one a workgroup.
 template <typename T>
 inline int64_t grad_partials(int64_t rows, int64_t n) {
     int64_t p = 0;
     with_grad_shape<T>(n, [&](auto tpr, auto) {
-        constexpr int TPR = decltype(tpr)::value;
-        p = grad_groups<TPR>(rows) * Shape<TPR>::rows;
+        p = grad_groups<decltype(tpr)::value>(rows);
         return hipSuccess;
     });
-    return rows == 1 ? 1 : p;
+    return p;
 }
 
 template <typename T>

@@ -106,7 +106,7 @@ __global__ __launch_bounds__(kPackThreads) void pack_kernel(MatvecArgs a, u32x4*
             v.load(a, row, o * 8);
             top = Max{}(top, v.top());
         }
-        top = block_reduce<kPackThreads / 64>(top, Max{}, tops);
+        top = block_reduce<kPackThreads>(top, Max{}, tops);
         if (top) {
             const int e = int(top >> 23), up = 141 - e < 126 ? 141 - e : 126;   // largest: 2^14 to 2^15
             factor = __builtin_bit_cast(float, uint32_t(127 + up) << 23);

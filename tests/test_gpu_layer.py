@@ -191,6 +191,28 @@ def test_norm_values_that_are_not_finite_and_extremes(scale):
     check_norm(x, None, w, 1e-6, scale, q, s, None, "f32")
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", ["block", "row"])
+@pytest.mark.parametrize("n", [8, 120, 128, 129, 200, 256, 257])
+def test_norm_short_rows_share_a_wavefront(dt, scale, n):
+    """Several rows to a wavefront, the last one of the launch not full; rows of
+    zeros, NaN and magnitudes that take the rescaled sum beside ordinary ones."""
+    import dense_linear_algebra_potrf_amd as bl
+    announce("rmsnorm_quant short rows", dt, scale, n)
+    ty = dtypes()[dt]
+    for rows in (1, 3, 37, 1030):
+        x, r, w = rand(rows, rows, n).to(ty), rand(rows + 1, rows, n).to(ty), (1 + 0.2 * rand(3, 1, n)[0]).to(ty)
+        r[:, 0] = 0
+        if rows > 3:
+            x[2], r[2] = 0, 0
+            x[5, n // 2] = float("nan")
+            x[9], r[9] = x[9] * 1e-25, 0
+            x[10], r[10] = x[10] * 1e20, 0
+            x[35], r[35] = x[35] * 1e25, 0
+        q, s, h = bl.rmsnorm_quant(x.cuda(), w.cuda(), r.cuda(), scale=scale, eps=1e-38)
+        check_norm(x, r, w, 1e-38, scale, q, s, h, dt)
+
+
 # ---------------------------------------------------------------- rmsnorm_grad
 
 def check_grad(dy, h, w, dh, eps, dx, dw, dt):
@@ -211,7 +233,8 @@ def check_grad(dy, h, w, dh, eps, dx, dw, dt):
 
 
 GRAD_SIZES = [(1, 1), (1, 700), (1, 4096), (2, 33), (3, 512), (5, 513), (9, 1024), (517, 1537), (6, 2049), (3, 4103),
-              (4, 8192), (2, 9001), (2, 16384), (2051, 64), (1100, 300)]
+              (4, 8192), (2, 9001), (2, 16384), (2051, 64), (1100, 300), (3000, 128), (129, 127), (65, 256), (1, 100), (33, 250),
+              (33000, 16)]
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
@@ -270,6 +293,24 @@ def test_grad_against_differences_of_the_forward():
         d[c] = step
         want = (loss(h64, w64 + d) - loss(h64, w64 - d)) / (2 * step)
         assert abs(want - float(dw[c])) <= 1e-4 * max(1, abs(want))
+
+
+@pytest.mark.parametrize("n", [100, 200, 700, 3000])
+def test_rows_of_zeros_with_an_eps_below_the_normal_range(n):
+    """1 / sqrt(eps) is an ordinary number, so the rows are zeros and their gradient dy w / sqrt(eps)."""
+    import torch
+    import dense_linear_algebra_potrf_amd as bl
+    for eps in (1e-38, 3e-44, 1e-30):
+        announce("rows of zeros", n, eps)
+        eps = float(np.float32(eps))
+        h, w, dy = torch.zeros(3, n), 1 + 0.2 * rand(1, 1, n)[0], rand(2, 3, n)
+        h[1] = 1e-22
+        for scale in ("block", "row"):
+            q, s, _ = bl.rmsnorm_quant(h.cuda(), w.cuda(), scale=scale, eps=eps)
+            check_norm(h, None, w, eps, scale, q, s, None, "f32")
+            assert not q[0].float().any()
+        dx, dw = bl.rmsnorm_grad(dy.cuda(), h.cuda(), w.cuda(), eps=eps)
+        check_grad(dy, h, w, None, eps, dx, dw, "f32")
 
 
 def test_grad_without_rows():

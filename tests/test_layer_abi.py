@@ -54,7 +54,7 @@ def test_rmsnorm_quant_refusals(lib, over, status, msg):
     assert msg in text
 
 
-GRAD = dict(type=0, rows=4, n=64, dy=P, lddy=64, h=P, ldh=64, w=P, dh=P, lddh=64, eps=1e-6, dx=P, lddx=64, dw=P,
+GRAD = dict(type=0, rows=400, n=64, dy=P, lddy=64, h=P, ldh=64, w=P, dh=P, lddh=64, eps=1e-6, dx=P, lddx=64, dw=P,
             workspace=P, bytes=1 << 30, stream=None)
 
 
