@@ -15,6 +15,15 @@
 // of the row's largest (their 8 and 4 significant bits fit in 11) and off by at
 // most 2^-40 of it below, far under the rounding of the 32-bit sums; the power is
 // taken off the results.
+//
+// What bounds it is the work in the compute unit: for 64 x 8192 x 8192 in groups of
+// 32 (25 us, of it 4.8 for the layout of x) the vector units are busy for 9.5 us
+// (scaling the sums 3.4, unpacking 2.3, the rest mostly before and after the loop),
+// the matrix cores for 3.4, and 1 MB of x goes from the L2 to each compute unit, 20
+// TB/s in all; the codes alone would take 7.  Groups of 128 take 22.5 us, 32 rows of
+// x 17.4.  Scaling the last group and unpacking the next one while a product runs
+// gained nothing (24.8), nor did codes from the cache (24.3): the two wavefronts of
+// a SIMD already overlap.
 #pragma once
 
 #include "weight_matvec_impl.hpp"
@@ -77,7 +86,9 @@ struct Octet {
 };
 
 // A workgroup for a row of x (of whole tiles of 16): its largest finite magnitude,
-// then 8 columns a thread at a time; the first kKept of them stay in registers.
+// then 8 columns a thread at a time; the first kKept of them (16384 columns) stay in
+// registers, so that such a row is read once.  4.8 us for 64 x 8192 in a launch of
+// its own, which is latency: 2 MB in and out would take 0.4.
 constexpr int kPackThreads = 512, kKept = 4;
 
 template <X XT, bool MIXED>
@@ -271,7 +282,10 @@ inline hipError_t weight_many_t(X xt, Type yt, const MatvecArgs& a, void* worksp
         return launch(weight_many_kernel<F, GROUP, MT, NB, WAVES>, grid, block, 0, s, a, static_cast<const u32x4*>(workspace),
                       static_cast<const float*>(row_scales(a, workspace)), xt, yt);
     };
-    // 32 rows of W to a workgroup where that leaves one for every compute unit
+    // 32 rows of W to a workgroup where that leaves one for every compute unit: x is read
+    // half as often (64 x 8192 x 8192 in groups of 32 25.2 us, 34.3 with 16; 32 x 28672 x
+    // 8192 53.8 and 68.8).  32 rows of x where there are no more (17 x 8192 x 8192 16.7 us,
+    // 19.3 as 64; 32 x 28672 x 8192 53.8 and 69.5).
     auto rows = [&](auto mt) {
         if (a.n >= 256 * 32) return tile(mt, ic<2>{}, ic<8>{});
         return tile(mt, ic<1>{}, ic<8>{});

@@ -1,16 +1,24 @@
-// Products of a few rows with 4-bit weights, y = x W^T, on the matrix cores.
+// Products of a few rows with 4-bit weights, y = x W^T, on the matrix cores:
+//     y[m, n] = sum over groups g of scale[n, g] (sum_k x u - z[n, g] sum_k x).
+//
+// HBM bounds it: the codes are read once, 1/4 of the bytes of 16-bit weights.  Up to
+// 16 rows of x cost what one does as long as the codes' stream hides the arithmetic,
+// which is why even one row goes over the matrix cores: on the vector units, with a
+// conversion, a scale and a multiplication per code and row, 1 x 28672 x 8192 took
+// 412 us.  Measured, with what a copy of those bytes would take:
+//     1 x 28672 x 8192, half precision, groups of 64, zero points  29.0 us (25.2)
+//     1 x 16384 x 8192, bfloat16, groups of 128                    13.6    (13.6)
+//     4 x 16384 x 4096, e4m3 blocks, e2m1 weights                   9.6    (7.0)
+//     16 x 8192 x 8192, bfloat16, groups of 128                    11.0    (6.9)
+//     1 x 4096 x 4096: 4.2 us in the kernel, 7.2 a call
 //
 // A wavefront multiplies 16 MB rows of x with 16 NB rows of W over chunks of
 // 128 columns; the wavefronts of a workgroup take every WAVES-th chunk and join
 // their sums in LDS, in a fixed order.
 //
-// Codes come as they lie in memory, 16 bytes (32 columns) a lane: lane (r, g),
-// r = lane % 16 the row of W and g = lane / 16, holds dwords 4 g .. 4 g + 3 of
-// the chunk.  A product of 16 x 16 x 32 wants 32 neighbouring columns over the
-// four g, so the dwords are transposed over g and register by the permlane
-// swaps (four instructions for 32 codes a lane); then product t covers columns
-// 32 t .. 32 t + 31, one group of scales (or a part of one), and x is read in
-// its natural order.
+// A product of 16 x 16 x 32 wants of lane (r, g), r = lane % 16 the row and g =
+// lane / 16, the columns 8 g .. 8 g + 7 of 32: product t of a chunk covers its
+// columns 32 t .. 32 t + 31, one group of scales or a part of one.
 //
 // Integer codes become 16-bit floats through the 8-bit conversion: the byte
 // 0000uuuu read as e4m3 is u 2^-9 for every u in 0..15, subnormal or not.  The
@@ -179,7 +187,9 @@ __device__ __forceinline__ double by_definition(const MatvecArgs& a, X xt, Forma
 
 // Scales and zero points of kGroups groups of TILE rows of W, in LDS as they lie
 // in memory; rows are padded so that 16 of them spread over the banks.  A chunk
-// has GROUPS groups.
+// has GROUPS groups.  Read from memory where they are used (two bytes of each of 16
+// rows a time) they cost more than the codes: 1 x 28672 x 8192 took 56 us, and 29
+// with no scales at all.
 template <Format F, int GROUPS, int TILE>
 struct Scales {
     static constexpr int SB = F == Format::FLOAT ? 1 : 2;       // bytes of a scale
@@ -299,8 +309,12 @@ __global__ __launch_bounds__(64 * WAVES) void weight_matvec_kernel(MatvecArgs a,
     const int rows_n = a.n - n0 < TILE ? int(a.n - n0) : TILE, rows_m = a.m - m0 < MT ? int(a.m - m0) : MT;
 
     // Loads a chunk that lies inside the row.  Codes: lane / 4 is the row, lane % 4
-    // the 16 bytes of it.  x: 64 / PER rows a load, PER lanes a row.  Rows past the
-    // end are not read: their results are not stored.
+    // the 16 bytes of it, so that a load takes whole lines; the transposition to the
+    // matrix cores' layout goes through LDS (16 x 8192 x 8192: 11 us, 14 with loads in
+    // that layout and the swaps of lanes).  x: 64 / PER rows a load, PER lanes a row.
+    // Rows past the end are not read: their results are not stored.  One chunk ahead:
+    // two and four took 9.0 and 9.5 us for 1 x 16384 x 4096, one 8.0 (the wavefronts
+    // of a compute unit are enough loads on their way, and registers fewer).
     constexpr int PER = ROW / 16, STEP = 64 / PER;
     const uint32_t code_at = uint32_t(lane >> 2) * uint32_t(a.ldc) + 16 * (lane & 3);
     const uint32_t x_at = uint32_t(lane / PER) * uint32_t(a.ldx * ES) + 16 * (lane % PER);
@@ -495,12 +509,20 @@ inline hipError_t weight_matvec_t(Type yt, Format f, int group, const MatvecArgs
     };
     constexpr int FEW = is_eight(XT) ? 8 : 4;                   // rows that one load holds
     auto shape = [&](auto fmt, auto size) {
-        const bool wide = a.n >= 256 * 32;                      // enough rows for every compute unit at 32 each
+        // 32 rows of W to a workgroup where that leaves one for every compute unit, since x
+        // and its fragments then serve twice (16 x 8192 x 8192 11.0 us, 13.4 with 16; 1 x
+        // 28672 x 8192 29.0 and 32.5).  Where 16 rows leave one workgroup or none for a
+        // compute unit, its wavefronts are twice as many (4 x 4096 x 14336 9.5 us, 10.8
+        // with 8; at 4096 columns the call's overhead hides both).
+        const bool wide = a.n >= 256 * 32;
         auto rows = [&](auto mt) {
             if (wide) return tile(fmt, size, mt, ic<2>{}, ic<8>{});
             if (a.n <= 256 * 16) return tile(fmt, size, mt, ic<1>{}, ic<16>{});
             return tile(fmt, size, mt, ic<1>{}, ic<8>{});
         };
+        // The matrix cores take 16 rows of x in any case; loading, holding and joining
+        // those that are there: 1 x 28672 x 8192 29.0 us (29.9 as 4 rows, 31.8 as 16), 4 x
+        // 4096 x 14336 9.5 (11.1 as 16).
         return a.m == 1 ? rows(ic<1>{}) : a.m <= FEW ? rows(ic<FEW>{}) : rows(ic<16>{});
     };
     if (f == Format::FLOAT) return shape(std::integral_constant<Format, Format::FLOAT>{}, ic<32>{});

@@ -5,6 +5,15 @@
 // DPP row, and its largest magnitude (or least and largest value) takes two to
 // four lane exchanges.  One pass: W is read once, the codes and values written
 // once.
+//
+//     float:    scale 2^e, the least e with max |w| <= 6 2^e;  code = e2m1(w / scale)
+//     integer:  scale = bf16(max |w| / 7);                    u = rint(w / scale) + 8
+//       zeros:  scale = bf16((max - min) / 15), both with 0;  u = rint(w / scale) + z
+//
+// HBM bounds it.  16384 x 8192 bf16 to e2m1 with the rounded values: 131 us, 4.65
+// TB/s; 4096 x 4096 f32 to integers with zero points and values: 33.5 us, 4.3 TB/s
+// (a large copy reaches 5.1).  The grid is one thread for every 8 columns: with four
+// rows to a thread the second took 35.1 us.
 #pragma once
 
 #include "layer_impl.hpp"
