@@ -10,10 +10,12 @@
 //     integer:  scale = bf16(max |w| / 7);                    u = rint(w / scale) + 8
 //       zeros:  scale = bf16((max - min) / 15), both with 0;  u = rint(w / scale) + z
 //
-// HBM bounds it.  16384 x 8192 bf16 to e2m1 with the rounded values: 131 us, 4.65
-// TB/s; 4096 x 4096 f32 to integers with zero points and values: 33.5 us, 4.3 TB/s
-// (a large copy reaches 5.1).  The grid is one thread for every 8 columns: with four
-// rows to a thread the second took 35.1 us.
+// HBM bounds it.  16384 x 8192 bf16 to e2m1 with the rounded values: 120 us, 5.1
+// TB/s, a large copy's rate (131 us with comparisons and selects in place of the
+// conversion instructions); 4096 x 4096 f32 to integers with zero points and values:
+// 33.2 us, 4.3 TB/s.  The grid is one thread for every 8 columns: with four rows to a
+// thread the second took 35.1 us, and 33.0 with a product with the reciprocal in place
+// of the division, and the division only next to a half.
 #pragma once
 
 #include "layer_impl.hpp"
@@ -26,19 +28,22 @@ using namespace layer;
 struct Least { __device__ __forceinline__ float operator()(float a, float b) const { return fminf(a, b); } };
 struct Most { __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); } };
 
-// The code of the e2m1 float next to t, |t| <= 6, ties to the even mantissa (0.25 -> 0, 0.75 -> 1, ..., 5 -> 4).
-__device__ __forceinline__ uint32_t e2m1_code(float t) {
-    const float v = fabsf(t);
-    const float steps = v < 2.0f ? rintf(v * 2.0f)            // 0, 0.5, 1, 1.5, (2): codes 0..4
-                        : v < 4.0f ? rintf(v) + 2.0f          // 2, 3, (4): codes 4..6
-                                   : rintf(v * 0.5f) + 4.0f;  // 4, 6: codes 6, 7
-    return uint32_t(steps) | (__builtin_bit_cast(uint32_t, t) >> 28 & 8u);
+// Eight floats of |t| <= 6 to the codes of the e2m1 floats next to them, ties to the
+// even mantissa (0.25 -> 0, 0.75 -> 1, ..., 5 -> 4), the first in the low half byte;
+// and back.  The conversion instructions' own scale stays 1: theirs is not defined
+// for a subnormal power of two.
+__device__ __forceinline__ uint32_t to_e2m1(const float (&t)[8]) {
+    uint32_t c = 0;
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, t[0], t[1], 1.0f, 0);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, t[2], t[3], 1.0f, 1);
+    c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, t[4], t[5], 1.0f, 2);
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, t[6], t[7], 1.0f, 3);
 }
-__device__ __forceinline__ float e2m1_value(uint32_t code) {
-    const uint32_t c = code & 7;
-    // exponent field c / 2 (bias 1), one mantissa bit; 0 and 1 are subnormal
-    const float v = c < 2 ? 0.5f * float(c) : __builtin_bit_cast(float, (126 + (c >> 1)) << 23 | (c & 1) << 22);
-    return code & 8 ? -v : v;
+__device__ __forceinline__ void from_e2m1(uint32_t c, float (&v)[8]) {
+    using pair = float __attribute__((ext_vector_type(2)));
+    const pair a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 1);
+    const pair d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 2), e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 3);
+    v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y, v[4] = d.x, v[5] = d.y, v[6] = e.x, v[7] = e.y;
 }
 
 template <typename T, Format F, int GROUP, bool ZEROS>
@@ -66,11 +71,11 @@ __global__ __launch_bounds__(256) void weight_quant_kernel(WeightQuantArgs a, in
             const uint32_t b = e2m1_scale_byte(top);
             const float up = power_of(b), down = power_of(b == 255 ? 255 : 254 - b);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint32_t u = finite ? e2m1_code(w[j] * down) : 0;
-                codes |= u << (4 * j);
-                value[j] = e2m1_value(u) * up;
-            }
+            for (int j = 0; j < 8; ++j) w[j] *= down;
+            codes = finite ? to_e2m1(w) : 0;
+            from_e2m1(codes, value);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) value[j] *= up;
             if (head) static_cast<uint8_t*>(a.scales)[row * a.lds + g] = uint8_t(b);
         } else {
             float span, z = 8;
