@@ -13,7 +13,7 @@
 // HBM bounds it.  16384 x 8192 bf16 to e2m1 with the rounded values: 120 us, 5.1
 // TB/s, a large copy's rate (131 us with comparisons and selects in place of the
 // conversion instructions); 4096 x 4096 f32 to integers with zero points and values:
-// 33.2 us, 4.3 TB/s.  The grid is one thread for every 8 columns: with four rows to a
+// 32.8 us, 4.4 TB/s.  The grid is one thread for every 8 columns: with four rows to a
 // thread the second took 35.1 us, and 33.0 with a product with the reciprocal in place
 // of the division, and the division only next to a half.
 #pragma once
@@ -24,9 +24,6 @@ namespace bl {
 namespace weight_quant_detail {
 
 using namespace layer;
-
-struct Least { __device__ __forceinline__ float operator()(float a, float b) const { return fminf(a, b); } };
-struct Most { __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); } };
 
 // Eight floats of |t| <= 6 to the codes of the e2m1 floats next to them, ties to the
 // even mantissa (0.25 -> 0, 0.75 -> 1, ..., 5 -> 4), the first in the low half byte;
@@ -56,14 +53,19 @@ __global__ __launch_bounds__(256) void weight_quant_kernel(WeightQuantArgs a, in
     for (int64_t row = (int64_t(blockIdx.y) << (8 - across)) + (threadIdx.x >> across); row < a.n; row += step) {
         const Raw8<T> wr = load8(static_cast<const T*>(a.W) + row * a.ldw + c, left);
         float w[8], value[8];
-        uint32_t top = 0;
+        // the largest magnitude, or those of the values above and below zero, as bits
+        // (a NaN is larger than all): one instruction a step
+        uint32_t top = 0, low = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             w[j] = wr[j];
-            top = Max{}(top, magnitude(w[j]));
+            const int32_t bits = __builtin_bit_cast(int32_t, w[j]), other = bits ^ INT32_MIN;
+            top = Max{}(top, ZEROS ? uint32_t(bits > 0 ? bits : 0) : magnitude(w[j]));
+            if constexpr (ZEROS) low = Max{}(low, uint32_t(other > 0 ? other : 0));
         }
         top = row_reduce<LANES>(top, Max{});
-        bool finite = top < kInfBits;
+        if constexpr (ZEROS) low = row_reduce<LANES>(low, Max{});
+        bool finite = top < kInfBits && low < kInfBits;
         uint32_t codes = 0;
         const int64_t g = c / GROUP;
         const bool head = (threadIdx.x & (LANES - 1)) == 0 && left > 0;
@@ -79,16 +81,9 @@ __global__ __launch_bounds__(256) void weight_quant_kernel(WeightQuantArgs a, in
             if (head) static_cast<uint8_t*>(a.scales)[row * a.lds + g] = uint8_t(b);
         } else {
             float span, z = 8;
-            [[maybe_unused]] float least = 0;
+            [[maybe_unused]] const float least = -__builtin_bit_cast(float, low);
             if constexpr (ZEROS) {
-                float most = 0;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    least = fminf(least, w[j]);
-                    most = fmaxf(most, w[j]);
-                }
-                least = row_reduce<LANES>(least, Least{});
-                most = row_reduce<LANES>(most, Most{});
+                const float most = __builtin_bit_cast(float, top);
                 span = (most - least) / 15.0f;
                 finite = finite && magnitude(span) < kInfBits;
             } else {
