@@ -43,6 +43,16 @@ __device__ __forceinline__ float rescale(uint32_t top) {
     return __builtin_bit_cast(float, uint32_t((e < -126 ? -126 : e < 100 ? e : 100) + 127) << 23);
 }
 
+// 1 / sqrt(mean): the instruction's result (an ulp off) and a step of Newton's method
+// with the products' own roundings, within half an ulp and a little; 0 and infinity,
+// for which the step is not a number, stay.
+__device__ __forceinline__ float inverse_root(float mean) {
+    const float y = __builtin_amdgcn_rsqf(mean);
+    const float t = mean * y, low = fmadd(mean, y, -t);
+    const float better = fmadd(0.5f * y, fmadd(-low, y, fmadd(-t, y, 1.0f)), y);
+    return better == better ? better : y;
+}
+
 template <typename T, int TPR, int VPT, bool BLOCK>
 __global__ __launch_bounds__(Shape<TPR>::threads) void rmsnorm_quant_kernel(NormQuantArgs a) {
     using S = Shape<TPR>;
@@ -69,8 +79,10 @@ __global__ __launch_bounds__(Shape<TPR>::threads) void rmsnorm_quant_kernel(Norm
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[i][j] = xr[j];
             }
+            float square = 0;                                   // short chains: small errors
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum = fmadd(v[i][j], v[i][j], sum);
+            for (int j = 0; j < 8; ++j) square = fmadd(v[i][j], v[i][j], square);
+            sum += square;
         }
         sum = block_reduce<TPR>(sum, Add{}, sums[0]);
         float mean = sum / float(n) + a.eps;
@@ -91,7 +103,7 @@ __global__ __launch_bounds__(Shape<TPR>::threads) void rmsnorm_quant_kernel(Norm
                 }
             mean = block_reduce<TPR>(sum, Add{}, sums[1]) / float(n) + a.eps * f * f;
         }
-        const float rs = __builtin_amdgcn_rsqf(mean);
+        const float rs = inverse_root(mean);
         uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
@@ -100,7 +112,10 @@ __global__ __launch_bounds__(Shape<TPR>::threads) void rmsnorm_quant_kernel(Norm
             uint32_t m = 0;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                v[i][j] = v[i][j] * rs * wr[j];
+                // h rs w rounded once: an output next to a tie of its 8 bits should fall on
+                // the definition's side
+                const float u = v[i][j] * rs, low = fmadd(v[i][j], rs, -u), wj = wr[j];
+                v[i][j] = fmadd(u, wj, low * wj);
                 // elements past the row's end are not part of it (0 * inf is not 0)
                 m = Max{}(m, j < left ? magnitude(v[i][j]) : 0u);
             }
@@ -118,7 +133,7 @@ __global__ __launch_bounds__(Shape<TPR>::threads) void rmsnorm_quant_kernel(Norm
             const float big = __builtin_bit_cast(float, top);
             const float scale = top >= kInfBits ? __builtin_nanf("") : fmaxf(big / kE4M3Max, kTiny);
             if (t == 0) static_cast<float*>(a.scales)[row] = scale;
-            const float inverse = 1.0f / scale;
+            const float inverse = top >= kInfBits ? scale : fminf(kE4M3Max / big, 0x1p126f);
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 const int c = 8 * (i * TPR + t);
@@ -182,6 +197,7 @@ __global__ __launch_bounds__(Shape<TPR>::threads) void rmsnorm_grad_kernel(NormG
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int c = 8 * (i * TPR + t), left = n - c;
+            float squares = 0, dots = 0;
             hr[i] = hn[i];
             gr[i] = gn[i];
             er[i] = en[i];
@@ -189,9 +205,11 @@ __global__ __launch_bounds__(Shape<TPR>::threads) void rmsnorm_grad_kernel(NormG
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float h = hr[i][j];
-                square = fmadd(h, h, square);
-                dot = fmadd(gr[i][j] * wr[j], h, dot);
+                squares = fmadd(h, h, squares);
+                dots = fmadd(gr[i][j] * wr[j], h, dots);
             }
+            square += squares;
+            dot += dots;
         }
         if (AHEAD && row + step < a.rows) load(row + step);
 #pragma unroll
@@ -226,7 +244,7 @@ __global__ __launch_bounds__(Shape<TPR>::threads) void rmsnorm_grad_kernel(NormG
             mean = square / float(n) + a.eps * f * f;
         }
         // with h f and rs = 1 / rms(h f): s = f rs, and h s = (h f) rs
-        const float rs = __builtin_amdgcn_rsqf(mean), s = f * rs;
+        const float rs = inverse_root(mean), s = f * rs;
         const float back = rs * (dot / float(n));
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
