@@ -674,7 +674,8 @@ def test_matvec_without_rows_and_refusals():
         big = torch.zeros(1, 40000, device="cuda")
         bl.rmsnorm_quant(big, big[0])
     with pytest.raises(bl.BatchlasError, match="workspace_bytes"):
-        bl.rmsnorm_grad(x, x, w, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        tall = x.repeat(100, 1)                       # more than one workgroup's rows
+        bl.rmsnorm_grad(tall, tall, w, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
 
 
 # ---------------------------------------------------------------- together
