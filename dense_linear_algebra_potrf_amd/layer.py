@@ -2,8 +2,8 @@
 operators"): argument checks and marshalling only, as in the package's other
 entry points.  Tensors here are row-major, [rows, columns], with any row stride.
 
-Every operator runs on the current stream, or on `stream`; tensors that it
-allocates belong to the current stream.
+Every operator runs on the current stream, or on `stream`, and tensors that it
+allocates (outputs, workspaces) belong to the stream that it runs on.
 """
 from __future__ import annotations
 
@@ -67,15 +67,19 @@ def _gpu(t) -> int:
     return at
 
 
-def _place(at: int, others, stream) -> int:
-    """The stream's handle, after checking that every tensor is on the current device, `at`."""
+def _on(stream, operator, *args, **kwargs):
+    """The operator with `stream` as the current one, so that what it allocates belongs to it."""
+    with torch.cuda.stream(stream):
+        return operator(*args, **kwargs)
+
+
+def _place(at: int, others) -> int:
+    """The current stream's handle, after checking that every tensor is on the current device, `at`."""
     for o in others:
         if o is not None and o.get_device() != at:
             raise ValueError("tensors must live on the GPU, on one device")
     if at != torch._C._cuda_getDevice():
         raise ValueError("tensors must live on the current device")
-    if stream is not None:
-        return int(stream.cuda_stream)
     return torch._C._cuda_getCurrentRawStream(at)
 
 
@@ -95,6 +99,9 @@ def rmsnorm_quant(x, weight, residual=None, *, eps: float = 1e-6, scale: str = "
     (scale="row"); h = x + residual in x's type (None without a residual).
     residual_out may be x or residual itself.
     """
+    if stream is not None:
+        return _on(stream, rmsnorm_quant, x, weight, residual, eps=eps, scale=scale, out=out,
+                   scales=scales, residual_out=residual_out)
     lib = _lib or _bind()
     ty = _float_type(x, "x")
     at = _gpu(x)
@@ -126,7 +133,7 @@ def rmsnorm_quant(x, weight, residual=None, *, eps: float = 1e-6, scale: str = "
         if scales is None:
             scales = x.new_empty(rows, dtype=torch.float32)
         _vector(scales, "scales", torch.float32, rows)
-    s = _place(at, (weight, residual, residual_out, out, scales), stream)
+    s = _place(at, (weight, residual, residual_out, out, scales))
     st = lib.batchlas_rmsnorm_quant(ty, _SCALES[scale], rows, n, x.data_ptr(), ldx, rp, ldr, w, eps,
                                     hp, ldh, out.data_ptr(), ldq, scales.data_ptr(), lds, s)
     if st:
@@ -144,6 +151,8 @@ def rmsnorm_grad(dy, h, weight, dh=None, *, eps: float = 1e-6, dx=None, dweight=
     or dh itself.  dweight=False: not computed.  workspace: a uint8 tensor of
     rmsnorm_grad_workspace(...) bytes, allocated by the call where it is None.
     """
+    if stream is not None:
+        return _on(stream, rmsnorm_grad, dy, h, weight, dh, eps=eps, dx=dx, dweight=dweight, workspace=workspace)
     lib = _lib or _bind()
     ty = _float_type(h, "h")
     at = _gpu(h)
@@ -167,7 +176,7 @@ def rmsnorm_grad(dy, h, weight, dh=None, *, eps: float = 1e-6, dx=None, dweight=
         if workspace is not None:
             size = workspace.numel()
             wp = _vector(workspace, "workspace", torch.uint8, size)
-    s = _place(at, (dy, weight, dh, dx, dweight if dp else None, workspace if wp else None), stream)
+    s = _place(at, (dy, weight, dh, dx, dweight if dp else None, workspace if wp else None))
     st = lib.batchlas_rmsnorm_grad(ty, rows, n, dy.data_ptr(), lddy, h.data_ptr(), ldh, w,
                                    None if dh is None else dh.data_ptr(), lddh, eps, dx.data_ptr(), lddx,
                                    dp, wp, size, s)
@@ -213,6 +222,9 @@ def weight_quant(W, *, format: str = "int4", group: int | None = None, zeros: bo
     values=True (or a tensor): also what the codes stand for, in W's type.
     zeros and values are None where they were not asked for.
     """
+    if stream is not None:
+        return _on(stream, weight_quant, W, format=format, group=group, zeros=zeros, values=values,
+                   codes=codes, scales=scales, zeros_out=zeros_out)
     lib = _lib or _bind()
     ty = _float_type(W, "W")
     at = _gpu(W)
@@ -247,7 +259,7 @@ def weight_quant(W, *, format: str = "int4", group: int | None = None, zeros: bo
     if values is not None:
         ldv = _rows(values, "values", W.dtype, (n, k))[2]
         vp = values.data_ptr()
-    s = _place(at, (codes, scales, zeros_out, values), stream)
+    s = _place(at, (codes, scales, zeros_out, values))
     st = lib.batchlas_weight_quant(ty, _FORMATS[format], group, n, k, W.data_ptr(), ldw, codes.data_ptr(), ldc,
                                    scales.data_ptr(), lds, zp, ldz, vp, ldv, s)
     if st:
@@ -265,6 +277,9 @@ def weight_matvec(x, codes, scales, zeros=None, *, format: str = "int4", group: 
     workspace: a uint8 tensor of weight_matvec_workspace(m, k) bytes (0 up to 16
     rows), allocated by the call where it is None.
     """
+    if stream is not None:
+        return _on(stream, weight_matvec, x, codes, scales, zeros, format=format, group=group,
+                   x_scales=x_scales, out=out, out_dtype=out_dtype, workspace=workspace)
     lib = _lib or _bind()
     xt = _TYPES.get(x.dtype, -1)
     if xt < 1:
@@ -308,7 +323,7 @@ def weight_matvec(x, codes, scales, zeros=None, *, format: str = "int4", group: 
         size = weight_matvec_workspace(m, k)
         workspace = x.new_empty(size, dtype=torch.uint8)
         wp = workspace.data_ptr()
-    s = _place(at, (codes, scales, zeros, x_scales, out, workspace), stream)
+    s = _place(at, (codes, scales, zeros, x_scales, out, workspace))
     st = lib.batchlas_weight_matvec(xt, xs, yt, _FORMATS[format], group, m, n, k, x.data_ptr(), ldx, xp, ldxs,
                                     codes.data_ptr(), ldc, scales.data_ptr(), lds, zp, ldz, out.data_ptr(), ldy, wp, size, s)
     if st:

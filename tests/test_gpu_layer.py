@@ -753,6 +753,33 @@ def test_runs_alike_on_another_stream_and_in_a_graph():
         assert all(torch.equal(a, b) for a, b in zip(eager, raw(out))), f"replay {rep}"
 
 
+def test_what_a_call_on_a_stream_allocates_belongs_to_it():
+    """Workspaces and outputs of calls that wait on a side stream are not handed out
+    again to work that runs meanwhile on the current one."""
+    import torch
+    import dense_linear_algebra_potrf_amd as bl
+    announce("allocations on a side stream")
+    s = layer_state(5)
+    kw = dict(group=64, x_scales=s["qs"])
+    layer_step(bl, s)
+    want = [bl.weight_matvec(s["q"], s["codes"], s["ws"], s["wz"], **kw), *bl.rmsnorm_grad(s["dy"], s["h"], s["w"], s["r"]),
+            *bl.rmsnorm_quant(s["x"], s["w"], s["r"]), *bl.weight_quant(s["W"], group=64, zeros=True, values=True)]
+    want = raw(want)
+    late, side = torch.zeros(1 << 24, device="cuda"), torch.cuda.Stream()
+    sizes = sorted({t.numel() for t in want} | {bl.weight_matvec_workspace(37, 1000), s["ws_grad"].numel()})
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(100):
+            late.add_(1)
+    got = [bl.weight_matvec(s["q"], s["codes"], s["ws"], s["wz"], stream=side, **kw),
+           *bl.rmsnorm_grad(s["dy"], s["h"], s["w"], s["r"], stream=side), *bl.rmsnorm_quant(s["x"], s["w"], s["r"], stream=side),
+           *bl.weight_quant(s["W"], group=64, zeros=True, values=True, stream=side)]
+    keep = [torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda") for size in sizes for _ in range(8)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, raw(got)))
+    assert all(bool((t == 0xFF).all()) for t in keep)
+
+
 def test_offsets_beyond_32_bits():
     """Arrays past 4 GiB: the last rows of a tall norm, of wide codes and of their products."""
     import torch
