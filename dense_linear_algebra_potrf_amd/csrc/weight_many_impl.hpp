@@ -141,6 +141,56 @@ __global__ __launch_bounds__(kPackThreads) void pack_kernel(MatvecArgs a, u32x4*
     }
 }
 
+// Joins the wavefronts' sums in their order (a lane's four of a tile of 16 x 16:
+// rows 4 (lane / 16) .. + 3 of x, column lane % 16), times the scale of x's row, and
+// stores y.  A wavefront takes a tile, with 16-byte reads; element by element, with
+// the row's scale from memory, 64 x 28672 x 8192 in groups of 128 took 76.9 us
+// instead of 72.9, and 64 x 28672 x 512 20.0 instead of 15.4.
+template <Format F, int GROUP, int MB, int NB, int WAVES>
+__device__ __forceinline__ void store_tiles(const MatvecArgs& a, X xt, Type yt, int64_t m0, int64_t n0, int rows_m, int rows_n,
+                                            int waves, const f32x4 (*sums)[MB * NB][64], const float* row_scale) {
+    const int lane = threadIdx.x & 63;
+    for (int tile = threadIdx.x >> 6; tile < MB * NB; tile += waves) {
+        const int ml = tile / NB * 16 + (lane >> 4) * 4, nl = tile % NB * 16 + (lane & 15);
+        f32x4 v = {0, 0, 0, 0};
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) {                       // those of wavefronts that are not there are not added
+            const f32x4 s = sums[w][tile][lane];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] += w < waves ? s[e] : 0.0f;
+        }
+        bool odd = false;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[e] = ml + e < rows_m && nl < rows_n ? v[e] * row_scale[ml + e] : 0;
+            odd = odd || magnitude(v[e]) >= kInfBits;
+        }
+        if (__ballot(odd)) {
+#pragma unroll 1
+            for (int e = 0; e < 4; ++e) {
+                float mine = e == 0 ? v[0] : e == 1 ? v[1] : e == 2 ? v[2] : v[3];
+#pragma unroll 1
+                for (uint64_t left = __ballot(magnitude(mine) >= kInfBits); left; left &= left - 1) {
+                    const int at = __builtin_ctzll(left);
+                    const double d = by_definition(a, xt, F, GROUP, m0 + tile / NB * 16 + (at >> 4) * 4 + e,
+                                                   n0 + tile % NB * 16 + (at & 15));
+                    if (lane == at) mine = float(d);
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v[q] = q == e ? mine : v[q];
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (ml + e >= rows_m || nl >= rows_n) continue;
+            const int64_t to = (m0 + ml + e) * a.ldy + n0 + nl;
+            if (yt == Type::F32) static_cast<float*>(a.y)[to] = v[e];
+            else if (yt == Type::F16) static_cast<f16*>(a.y)[to] = f16(v[e]);
+            else static_cast<bf16*>(a.y)[to] = bf16(v[e]);
+        }
+    }
+}
+
 template <Format F, int GROUP, int MT, int NB, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void weight_many_kernel(MatvecArgs a, const u32x4* packed, const float* row_scale,
                                                                      X xt, Type yt) {
@@ -148,8 +198,9 @@ __global__ __launch_bounds__(64 * WAVES) void weight_many_kernel(MatvecArgs a, c
     __shared__ Scales<F, GROUPS, TILE> scales;
     __shared__ union {
         u32x4 codes[WAVES][NB * 64];
-        float sums[WAVES][MB * NB * 4][64];
+        f32x4 sums[WAVES][MB * NB][64];
     } lds;
+    __shared__ float factor[MT];                                // of x's rows
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int waves = blockDim.x >> 6, r = lane & 15, g = lane >> 4;
@@ -192,6 +243,7 @@ __global__ __launch_bounds__(64 * WAVES) void weight_many_kernel(MatvecArgs a, c
 #pragma unroll
         for (int j = 0; j < NB; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 
+    if (threadIdx.x < rows_m) factor[threadIdx.x] = row_scale[m0 + threadIdx.x];
     constexpr int PHASE = kGroups / GROUPS;
     u32x4 held[NB] = {};
     Frag x[MB][4];
@@ -260,11 +312,9 @@ __global__ __launch_bounds__(64 * WAVES) void weight_many_kernel(MatvecArgs a, c
 #pragma unroll
     for (int i = 0; i < MB; ++i)
 #pragma unroll
-        for (int j = 0; j < NB; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) lds.sums[wave][(i * NB + j) * 4 + e][lane] = acc[i][j][e];
+        for (int j = 0; j < NB; ++j) lds.sums[wave][i * NB + j][lane] = acc[i][j];
     __syncthreads();
-    store_sums<F, GROUP, MB, NB>(a, xt, yt, m0, n0, rows_m, rows_n, waves, &lds.sums[0], row_scale);
+    store_tiles<F, GROUP, MB, NB, WAVES>(a, xt, yt, m0, n0, rows_m, rows_n, waves, &lds.sums[0], factor);
 }
 
 // x's layout in the workspace: the tiles, then the rows' scales.
@@ -284,9 +334,16 @@ inline hipError_t weight_many_t(X xt, Type yt, const MatvecArgs& a, void* worksp
     };
     // 32 rows of W to a workgroup where that leaves one for every compute unit: x is read
     // half as often (64 x 8192 x 8192 in groups of 32 25.2 us, 34.3 with 16; 32 x 28672 x
-    // 8192 53.8 and 68.8).  32 rows of x where there are no more (17 x 8192 x 8192 16.7 us,
-    // 19.3 as 64; 32 x 28672 x 8192 53.8 and 69.5).
+    // 8192 53.8 and 68.8).  With 64 rows of x a compute unit has the registers and LDS of
+    // one workgroup of 8 wavefronts, and waits while it starts and joins: two of 4 where
+    // there are so many (64 x 28672 x 8192 76.9 us, 84.3 with 8; 64 x 16384 x 4096 23.2 and
+    // 26.1; 64 x 28672 x 512 20.0 and 35.0).  32 rows of x leave room for several (32 x 16384
+    // x 8192 26.1 us, 29.0 with 4).
+    // 32 rows of x where there are no more (17 x 8192 x 8192 16.7 us, 19.3 as 64; 32 x 28672
+    // x 8192 53.8 and 69.5).
     auto rows = [&](auto mt) {
+        if constexpr (decltype(mt)::value == 64)
+            if (a.n >= 512 * 32) return tile(mt, ic<2>{}, ic<4>{});
         if (a.n >= 256 * 32) return tile(mt, ic<2>{}, ic<8>{});
         return tile(mt, ic<1>{}, ic<8>{});
     };
