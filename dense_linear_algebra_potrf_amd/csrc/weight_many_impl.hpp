@@ -31,8 +31,6 @@
 namespace bl {
 namespace weight_matvec_detail {
 
-using f16x2 = f16 __attribute__((ext_vector_type(2)));
-
 // Eight bytes at p, of which `left` belong to the row; the others are zero.
 __device__ __forceinline__ uint64_t load_octet(const uint8_t* p, int left) {
     uint64_t e = 0;
@@ -266,30 +264,23 @@ __global__ __launch_bounds__(64 * WAVES) void weight_many_kernel(MatvecArgs a, c
             for (int i = 0; i < NB; ++i) own[64 * i + (lane & ~3) + ((lane & 3) ^ (lane >> 4))] = held[i];
             load_codes(next, held);
             wave_lds_sync();
-            float scale[NB][GROUPS], zeros[NB][GROUPS];
+            float scale[NB][GROUPS];
+            uint32_t zeros[NB][GROUPS];
 #pragma unroll
             for (int j = 0; j < NB; ++j) scales.get(16 * j + r, group, scale[j], zeros[j]);
 #pragma unroll
             for (int s = 0; s < GROUPS; ++s) {
                 f32x4 part[MB][NB];
-                f16x2 zero[NB];
 #pragma unroll
-                for (int j = 0; j < NB; ++j) {
-                    const f16 z = f16(zeros[j][s]);
-                    zero[j] = f16x2{z, z};
+                for (int j = 0; j < NB; ++j)
 #pragma unroll
                     for (int i = 0; i < MB; ++i) part[i][j] = f32x4{0, 0, 0, 0};
-                }
 #pragma unroll
                 for (int q = 0; q < STEPS; ++q) {
                     const int t = s * STEPS + q;
 #pragma unroll
                     for (int j = 0; j < NB; ++j) {
-                        Frag w = unpack<true, F, true>(get_codes(j, t));
-                        if constexpr (F == Format::INTEGER) {
-#pragma unroll
-                            for (uint32_t& v : w.word) v = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, v) - zero[j]);
-                        }
+                        const Frag w = unpack<true, F>(get_codes(j, t), Zero<true>(zeros[j][s]));
 #pragma unroll
                         for (int i = 0; i < MB; ++i) part[i][j] = product<true>(x[i][t], w, part[i][j]);
                     }

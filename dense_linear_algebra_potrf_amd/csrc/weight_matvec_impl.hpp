@@ -1,5 +1,5 @@
 // Products of a few rows with 4-bit weights, y = x W^T, on the matrix cores:
-//     y[m, n] = sum over groups g of scale[n, g] (sum_k x u - z[n, g] sum_k x).
+//     y[m, n] = sum over groups g of scale[n, g] sum_k x (u - z[n, g]).
 //
 // HBM bounds it: the codes are read once, 1/4 of the bytes of 16-bit weights.  Up to
 // 16 rows of x cost what one does as long as the codes' stream hides the arithmetic,
@@ -20,15 +20,17 @@
 // lane / 16, the columns 8 g .. 8 g + 7 of 32: product t of a chunk covers its
 // columns 32 t .. 32 t + 31, one group of scales or a part of one.
 //
-// Integer codes become 16-bit floats through the 8-bit conversion: the byte
-// 0000uuuu read as e4m3 is u 2^-9 for every u in 0..15, subnormal or not.  The
-// product takes u as it is, and z times the sum of x over the group, from a
-// product with ones, is taken off afterwards.  Scales are applied to the sums in
-// 32 bits.
+// An integer code is put, where it lies, into the bits of a half-precision float
+// 1024 + u or 64 + u, two at a time, and the float less 1024 + z or 64 + z is u - z:
+// packed in half precision, for bfloat16 (which has no packed sums) by an fma from
+// half precision to 32 bits each.  All of it is exact, so the zero point is off
+// before the product.  Taken off the sums instead (z times the sum of x) it costs
+// less, but a large x whose weight is zero then stands in both sums and takes the
+// bits of the others with it.  Scales are applied to the sums in 32 bits.
 //
-// The detours (codes without their scale, codes without their zero point) give
-// the definition's result wherever they are finite.  Where they are not, the
-// element is computed again from the definition in 64 bits.
+// The codes go without their scale, so a sum may leave the range of 32 bits where
+// the definition's does not.  What is not finite is computed again from the
+// definition in 64 bits.
 #pragma once
 
 #include "layer_impl.hpp"
@@ -40,6 +42,7 @@ using namespace layer;
 
 using bf16x8 = bf16 __attribute__((ext_vector_type(8)));
 using f16x8 = f16 __attribute__((ext_vector_type(8)));
+using f16x2 = f16 __attribute__((ext_vector_type(2)));
 using f32x4 = float __attribute__((ext_vector_type(4)));
 using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
 
@@ -66,11 +69,20 @@ __device__ __forceinline__ f32x4 product(const Frag& a, const Frag& b, f32x4 c) 
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-template <bool HALF>
-__device__ __forceinline__ Frag ones_of() {
-    constexpr uint32_t one = HALF ? 0x3c003c00u : 0x3f803f80u;
-    return Frag{{one, one, one, one}};
-}
+// What makes u - z of a code's float: less 1024 + z, or 64 + z; z is a byte.  In
+// bfloat16 the integers are kept as halves (an fma with a factor of one would become
+// a conversion and a sum).
+template <bool HALF> struct Zero {
+    f16x2 low, high;
+    __device__ __forceinline__ explicit Zero(uint32_t z)
+        : low(__builtin_bit_cast(f16x2, (z | z << 16) + 0x64006400u)), high(low - f16x2{f16(960.0f), f16(960.0f)}) {}
+};
+template <> struct Zero<false> {
+    float low, high;
+    __device__ __forceinline__ explicit Zero(uint32_t z) : low(-0.5f * float(z) - 512.0f), high(low + 480.0f) {}
+};
+// What a distance of 1 from the zero point stands for, over the scale.
+template <bool HALF, Format F> constexpr float kUnit = !HALF && F == Format::INTEGER ? 2.0f : 1.0f;
 
 template <bool HALF>
 __device__ __forceinline__ Frag from_e4m3(uint32_t lo, uint32_t hi, float scale) {
@@ -89,10 +101,10 @@ __device__ __forceinline__ Frag from_e4m3(uint32_t lo, uint32_t hi, float scale)
     return f;
 }
 
-// Codes of 8 columns (a dword) as floats, integers as they are (0..15) and in
-// the order of their half bytes (MIXED: 0 2 4 6 1 3 5 7) or in that of the columns.
-template <bool HALF, Format F, bool MIXED>
-__device__ __forceinline__ Frag unpack(uint32_t w) {
+// Codes of 8 columns (a dword) as floats over kUnit, integers less their zero point
+// and in the order in which they come apart: 0 4 1 5 2 6 3 7.
+template <bool HALF, Format F>
+__device__ __forceinline__ Frag unpack(uint32_t w, [[maybe_unused]] const Zero<HALF>& zero) {
     Frag f;
     if constexpr (F == Format::FLOAT) {
         if constexpr (HALF) {
@@ -107,20 +119,32 @@ __device__ __forceinline__ Frag unpack(uint32_t w) {
             f.word[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 3));
         }
     } else {
-        const uint32_t even = w & 0x0f0f0f0fu, odd = w >> 4 & 0x0f0f0f0fu;
-        if constexpr (MIXED) f = from_e4m3<HALF>(even, odd, 512.0f);
-        else f = from_e4m3<HALF>(__builtin_amdgcn_perm(odd, even, 0x05010400u), __builtin_amdgcn_perm(odd, even, 0x07030602u), 512.0f);
+        // half bytes 0 and 4 (1 and 5) of v: a step of the float 1024 is 1, of 64 it is 1 / 16
+        uint32_t low = 0x64006400u, high = 0x54005400u, low_bits = 0x000f000fu, high_bits = 0x00f000f0u;
+        asm("" : "+v"(low), "+v"(high), "+s"(low_bits), "+s"(high_bits));   // in registers: the mask and the float in one instruction
+        auto pair = [&](uint32_t v, bool is_high) {
+            const f16x2 u = __builtin_bit_cast(f16x2, is_high ? (v & high_bits) | high : (v & low_bits) | low);
+            if constexpr (HALF) {
+                return __builtin_bit_cast(uint32_t, u - (is_high ? zero.high : zero.low));
+            } else {
+                // small integers: the upper halves of their floats are all of them
+                const float off = is_high ? zero.high : zero.low, a = fmadd(float(u.x), 0.5f, off), b = fmadd(float(u.y), 0.5f, off);
+                return uint32_t(__builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, b), __builtin_bit_cast(uint32_t, a), 0x07060302u));
+            }
+        };
+        f.word[0] = pair(w, false), f.word[1] = pair(w, true);
+        f.word[2] = pair(w >> 8, false), f.word[3] = pair(w >> 8, true);
     }
     return f;
 }
 
-// Columns 0..7 in the order 0 2 4 6 1 3 5 7, for each 8 of a piece.
+// Columns 0..7 in the order 0 4 1 5 2 6 3 7, for each 8 of a piece.
 template <bool EIGHT>
 __device__ __forceinline__ u32x4 mixed(u32x4 v) {
-    constexpr uint32_t LO = EIGHT ? 0x06040200u : 0x05040100u, HI = EIGHT ? 0x07050301u : 0x07060302u;
+    constexpr uint32_t LO = EIGHT ? 0x05010400u : 0x05040100u, HI = EIGHT ? 0x07030602u : 0x07060302u;
     auto perm = [](uint32_t a, uint32_t b, uint32_t s) { return uint32_t(__builtin_amdgcn_perm(a, b, s)); };
     if constexpr (EIGHT) return u32x4{perm(v[1], v[0], LO), perm(v[1], v[0], HI), perm(v[3], v[2], LO), perm(v[3], v[2], HI)};
-    else return u32x4{perm(v[1], v[0], LO), perm(v[3], v[2], LO), perm(v[1], v[0], HI), perm(v[3], v[2], HI)};
+    else return u32x4{perm(v[2], v[0], LO), perm(v[2], v[0], HI), perm(v[3], v[1], LO), perm(v[3], v[1], HI)};
 }
 
 // `bytes` (of elements of ES bytes) of 16 at p, the others zero: of a row that is
@@ -230,7 +254,7 @@ struct Scales {
     }
 
     // Those of a row's groups from `group` on, a multiple of GROUPS.
-    __device__ __forceinline__ void get(int row, int group, float (&s)[GROUPS], float (&z)[GROUPS]) const {
+    __device__ __forceinline__ void get(int row, int group, float (&s)[GROUPS], uint32_t (&z)[GROUPS]) const {
         uint64_t v = 0;
         __builtin_memcpy(&v, __builtin_assume_aligned(&scale[row][group * SB], GROUPS * SB), GROUPS * SB);
         uint32_t w = 0;
@@ -240,7 +264,7 @@ struct Scales {
             if constexpr (SB == 2) {
                 const uint32_t half = uint32_t(v >> (32 * (i / 2)));
                 s[i] = __builtin_bit_cast(float, i & 1 ? half & 0xffff0000u : half << 16);
-                z[i] = float(w >> (8 * i) & 255u);
+                z[i] = w >> (8 * i) & 255u;
             } else {
                 // 2^128, infinity, for a byte of 255: the sum is then not finite, and NaN by the definition
                 s[i] = __builtin_amdgcn_ldexpf(1.0f, int(uint32_t(v) >> (8 * i) & 255u) - 127);
@@ -250,11 +274,11 @@ struct Scales {
     }
 };
 
-// Joins the wavefronts' sums (slot of four rows by lane), times the scale of x's
-// row if there is one, and stores the tile's y.
+// Joins the wavefronts' sums (slot of four rows by lane), times `unit` and the scale
+// of x's row if there is one, and stores the tile's y.
 template <Format F, int GROUP, int MB, int NB>
 __device__ __forceinline__ void store_sums(const MatvecArgs& a, X xt, Type yt, int64_t m0, int64_t n0, int rows_m, int rows_n,
-                                           int waves, const float (*sums)[MB * NB * 4][64], const float* row_scale) {
+                                           int waves, const float (*sums)[MB * NB * 4][64], float unit, const float* row_scale) {
     constexpr int TILE = 16 * NB;
     const int lane = threadIdx.x & 63;
     // whole wavefronts: the detour below takes all lanes
@@ -266,6 +290,7 @@ __device__ __forceinline__ void store_sums(const MatvecArgs& a, X xt, Type yt, i
         float v = 0;
         if (in) {
             for (int w = 0; w < waves; ++w) v += sums[w][slot][from];
+            v *= unit;
             if (row_scale) v *= row_scale[m];
         }
         for (uint64_t odd = __ballot(magnitude(v) >= kInfBits); odd; odd &= odd - 1) {
@@ -285,15 +310,12 @@ template <X XT, Format F, int GROUP, int MT, int NB, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void weight_matvec_kernel(MatvecArgs a, Type yt) {
     constexpr bool HALF = in_half(XT), EIGHT = is_eight(XT);
     constexpr int MB = (MT + 15) / 16;                          // tiles of 16 rows of x, the last partly empty
-    constexpr bool OFFSET = F == Format::INTEGER;               // zero points are taken off the sums
     constexpr int GROUPS = kChunk / GROUP, STEPS = GROUP / 32;  // groups of a chunk, products of a group
     constexpr int TILE = 16 * NB;                               // rows of W
     constexpr int ES = EIGHT ? 1 : 2, ROW = kChunk * ES;        // bytes of an element and a chunk's row of x
     constexpr int SLOTS = ROW / 16;                             // of 16 bytes
     using H = Held<XT, MT, NB>;
-    // integers come apart in a mixed order: x is mixed alike on its way into LDS,
-    // or the codes on their way out of it, whichever is less
-    constexpr bool MIXED = F == Format::INTEGER && 4 * H::PIECES <= 8 * NB;
+    constexpr bool MIXED = F == Format::INTEGER;                // x as the codes come apart, on its way into LDS
     constexpr int SUMS = MT < 4 ? MT : 4;                       // of a lane's four sums, those of rows of x
     __shared__ Scales<F, GROUPS, TILE> scales;                  // of the groups at hand
     __shared__ union {
@@ -425,31 +447,26 @@ __global__ __launch_bounds__(64 * WAVES) void weight_matvec_kernel(MatvecArgs a,
         for (int i = 0; i < MB; ++i) xscale[i] = XT == X::F8_BLOCK ? d.xscale[i] : 0;
         if (next < full) load(next, d);
         wave_lds_sync();
-        float scale[NB][GROUPS], zero[NB][GROUPS];
+        float scale[NB][GROUPS];
+        uint32_t zero[NB][GROUPS];
 #pragma unroll
         for (int j = 0; j < NB; ++j) scales.get(16 * j + r, group, scale[j], zero[j]);
 #pragma unroll
         for (int s = 0; s < GROUPS; ++s) {
-            f32x4 part[MB][NB], ones[MB];
+            f32x4 part[MB][NB];
 #pragma unroll
-            for (int i = 0; i < MB; ++i) {
-                ones[i] = f32x4{0, 0, 0, 0};
+            for (int i = 0; i < MB; ++i)
 #pragma unroll
                 for (int j = 0; j < NB; ++j) part[i][j] = f32x4{0, 0, 0, 0};
-            }
 #pragma unroll
             for (int q = 0; q < STEPS; ++q) {
                 const int t = s * STEPS + q;
                 Frag x[MB];
 #pragma unroll
-                for (int i = 0; i < MB; ++i) {
-                    x[i] = get_x(i, t, xscale[i]);
-                    if constexpr (OFFSET)
-                        ones[i] = product<HALF>(x[i], ones_of<HALF>(), ones[i]);
-                }
+                for (int i = 0; i < MB; ++i) x[i] = get_x(i, t, xscale[i]);
 #pragma unroll
                 for (int j = 0; j < NB; ++j) {
-                    const Frag w = unpack<HALF, F, MIXED>(get_codes(j, t));
+                    const Frag w = unpack<HALF, F>(get_codes(j, t), Zero<HALF>(zero[j][s]));
 #pragma unroll
                     for (int i = 0; i < MB; ++i) part[i][j] = product<HALF>(x[i], w, part[i][j]);
                 }
@@ -459,10 +476,7 @@ __global__ __launch_bounds__(64 * WAVES) void weight_matvec_kernel(MatvecArgs a,
 #pragma unroll
                 for (int i = 0; i < MB; ++i)
 #pragma unroll
-                    for (int e = 0; e < SUMS; ++e) {
-                        const float p = OFFSET ? fmadd(-zero[j][s], ones[i][e], part[i][j][e]) : part[i][j][e];
-                        acc[i][j][e] = fmadd(scale[j][s], p, acc[i][j][e]);
-                    }
+                    for (int e = 0; e < SUMS; ++e) acc[i][j][e] = fmadd(scale[j][s], part[i][j][e], acc[i][j][e]);
             }
         }
     };
@@ -493,7 +507,7 @@ __global__ __launch_bounds__(64 * WAVES) void weight_matvec_kernel(MatvecArgs a,
             for (int e = 0; e < SUMS; ++e) lds.sums[wave][(i * NB + j) * 4 + e][lane] = acc[i][j][e];
     __syncthreads();
 
-    store_sums<F, GROUP, MB, NB>(a, XT, yt, m0, n0, rows_m, rows_n, waves, &lds.sums[0],
+    store_sums<F, GROUP, MB, NB>(a, XT, yt, m0, n0, rows_m, rows_n, waves, &lds.sums[0], kUnit<HALF, F>,
                                 XT == X::F8_ROW ? static_cast<const float*>(a.xscales) : nullptr);
 }
 
@@ -504,8 +518,12 @@ inline hipError_t weight_matvec_t(Type yt, Format f, int group, const MatvecArgs
         constexpr int MT = decltype(mt)::value, NB = decltype(nb)::value, WAVES = decltype(waves)::value;
         const dim3 block(uint32_t(64 * (chunks < WAVES ? chunks : WAVES)));
         const dim3 grid(uint32_t((a.n + 16 * NB - 1) / (16 * NB)), uint32_t((a.m + MT - 1) / MT));
-        return launch(weight_matvec_kernel<XT, decltype(fmt)::value, decltype(size)::value, MT, NB, WAVES>, grid, block, 0, s,
-                      a, yt);
+        // One row, 32 rows of W: LDS that is not used keeps a compute unit at two workgroups.
+        // A third one takes 1 x 28672 x 8192 in half precision and groups of 64 from 29.3 to
+        // 32.2 us and 32768 rows of W from 32.9 to 35.3; 20480 of them gain (20.0 to 19.1).
+        constexpr size_t unused = decltype(fmt)::value == Format::INTEGER && MT == 1 && NB == 2 ? 16384 : 0;
+        return launch(weight_matvec_kernel<XT, decltype(fmt)::value, decltype(size)::value, MT, NB, WAVES>, grid, block, unused,
+                      s, a, yt);
     };
     constexpr int FEW = is_eight(XT) ? 8 : 4;                   // rows that one load holds
     auto shape = [&](auto fmt, auto size) {

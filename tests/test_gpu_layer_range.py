@@ -1,0 +1,82 @@
+"""Products with 4-bit weights on x of a wide range, against the definition in 64
+bits and with a bound that follows |x| |w| (not |x| times the codes).
+
+The bound, from the arithmetic (u = 2^-24): codes less their zero point and x are
+exact in 16 bits, so their products are exact in 32.  A product of the matrix
+cores adds 32 of them to a sum with at most 32 roundings of 2 u each (should it
+cut off); up to 4 of them make a group, whose sum takes one rounding with its
+scale; a wavefront adds its groups in turn, at most 16 wavefronts are joined, and
+4 roundings are left for the scale of x's row and the output:
+    (4 * 32 * 2 + groups + 16 + 4) u  of  sum |x| |w|.
+"""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+from tests import _layer_ref as ref
+from tests._gpu import announce
+from tests.test_gpu_layer import FORMS, SUBNORMAL, U, dtypes, make_weights
+
+pytestmark = pytest.mark.gpu
+
+
+def bound(x64, W, groups: int) -> np.ndarray:
+    return (4 * 32 * 2 + groups + 20) * U * (np.abs(x64) @ np.abs(W).T) + (groups + 20) * SUBNORMAL["f32"]
+
+
+def wide_x(kind, m, k, column, seed):
+    """(x in 64 bits, GPU x, GPU x_scales): ordinary values, and one column that dwarfs them by 2^14 and more."""
+    import torch
+    g = torch.Generator().manual_seed(seed)
+    v = torch.randn(m, k, generator=g)
+    if kind in ("bf16", "f16"):
+        if kind == "bf16":
+            v[:, column] = 2.0 ** torch.tensor([14, 22, 31, 40, 60, 100])[torch.arange(m) % 6].float()
+        else:
+            v *= 2.0 ** -8
+            v[:, column] = torch.tensor([1e3, 6e4])[torch.arange(m) % 2]
+        x = v.to(dtypes()[kind])
+        return ref.f64(x), x.cuda(), None
+    v = (v * 2.0 ** -6).clamp(-1, 1)
+    v[:, column] = 448.0
+    if kind == "f8row":
+        q, s = v.to(torch.float8_e4m3fn), 0.5 + torch.rand(m, generator=g)
+        return ref.f64(q.float()) * ref.f64(s)[:, None], q.cuda(), s.cuda()
+    at = column // 32
+    own = v[:, column].clone()
+    v[:, 32 * at:32 * at + 32] = 0                  # the large column is alone in its block of scales
+    v[:, column] = own
+    q = v.to(torch.float8_e4m3fn)
+    b = torch.randint(125, 129, (m, -(-k // 32)), generator=g, dtype=torch.uint8)
+    b[:, at] = torch.tensor([127, 140, 160, 200])[torch.arange(m) % 4].to(torch.uint8)
+    wide = np.repeat(2.0 ** (b.double().numpy() - 127), 32, 1)[:, :k]
+    return ref.f64(q.float()) * wide, q.cuda(), b.view(torch.float8_e8m0fnu).cuda()
+
+
+def check_large_column(kind, fmt, group, zeros, rows):
+    import torch
+    import dense_linear_algebra_potrf_amd as bl
+    n, k = 33, 300
+    for i, m in enumerate(rows):
+        for column in (5, 131, 299):
+            announce("weight_matvec large column", kind, fmt, group, zeros, m, column)
+            codes, sc, z, (_, cs, cz) = make_weights(i, n, k, fmt, group, zeros)
+            codes[:30, column] = 0 if fmt == "fp4" else 8 if z is None else z[:30, column // group]
+            x64, x, xs = wide_x(kind, m, k, column, i)
+            W = ref.held(codes, sc, z, fmt, group, k)
+            assert not W[:30, column].any()
+            y = bl.weight_matvec(x, torch.from_numpy(ref.pack(codes)).cuda(), cs, cz, format=fmt, group=group, x_scales=xs,
+                                 out_dtype=torch.float32)
+            off, most = np.abs(ref.f64(y) - x64 @ W.T), bound(x64, W, -(-k // group))
+            assert (off <= most).all(), float((off / most).max())
+
+
+KINDS = ["bf16", "f16", "f8block", "f8row"]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("fmt,group,zeros", FORMS)
+def test_a_large_column_without_weight_leaves_the_others(kind, fmt, group, zeros):
+    """Up to 16 rows of x: a column whose weights are zero adds nothing, however large it is."""
+    check_large_column(kind, fmt, group, zeros, (1, 4, 7, 16))
