@@ -81,8 +81,17 @@ template <> struct Zero<false> {
     float low, high;
     __device__ __forceinline__ explicit Zero(uint32_t z) : low(-0.5f * float(z) - 512.0f), high(low + 480.0f) {}
 };
-// What a distance of 1 from the zero point stands for, over the scale.
-template <bool HALF, Format F> constexpr float kUnit = !HALF && F == Format::INTEGER ? 2.0f : 1.0f;
+// The scale of a block of 8-bit x, times 8, so that the smallest value of the smallest
+// scale, 2^-9 2^-127, is a multiple of bfloat16's smallest step (2^-133), and the
+// conversion instruction gets no subnormal scale; NaN where that is beyond 2^127, so
+// that the element is computed again in 64 bits, and for a byte of 255.
+__device__ __forceinline__ float block_power(uint32_t b) {
+    return __builtin_bit_cast(float, b < 252 ? (b + 3) << 23 : 0x7fc00000u);
+}
+// What the sums are multiplied by: integers in bfloat16 are halves, block-scaled x is
+// eight times what it stands for.
+template <X XT, Format F>
+constexpr float kUnit = (!in_half(XT) && F == Format::INTEGER ? 2.0f : 1.0f) * (XT == X::F8_BLOCK ? 0.125f : 1.0f);
 
 template <bool HALF>
 __device__ __forceinline__ Frag from_e4m3(uint32_t lo, uint32_t hi, float scale) {
@@ -101,8 +110,8 @@ __device__ __forceinline__ Frag from_e4m3(uint32_t lo, uint32_t hi, float scale)
     return f;
 }
 
-// Codes of 8 columns (a dword) as floats over kUnit, integers less their zero point
-// and in the order in which they come apart: 0 4 1 5 2 6 3 7.
+// Codes of 8 columns (a dword) as floats, integers less their zero point (in
+// bfloat16 half of that) and in the order in which they come apart: 0 4 1 5 2 6 3 7.
 template <bool HALF, Format F>
 __device__ __forceinline__ Frag unpack(uint32_t w, [[maybe_unused]] const Zero<HALF>& zero) {
     Frag f;
@@ -424,7 +433,7 @@ __global__ __launch_bounds__(64 * WAVES) void weight_matvec_kernel(MatvecArgs a,
         const uint32_t* p = reinterpret_cast<const uint32_t*>(&own.x[row * SLOTS + (byte / 16 ^ mix(row))]);
         if constexpr (EIGHT) {
             const uint2 v = reinterpret_cast<const uint2*>(p)[g & 1];
-            return from_e4m3<HALF>(v.x, v.y, XT == X::F8_BLOCK ? power_of(scale >> (8 * t) & 255u) : 1.0f);
+            return from_e4m3<HALF>(v.x, v.y, XT == X::F8_BLOCK ? block_power(scale >> (8 * t) & 255u) : 1.0f);
         } else {
             return *reinterpret_cast<const Frag*>(p);
         }
@@ -507,7 +516,7 @@ __global__ __launch_bounds__(64 * WAVES) void weight_matvec_kernel(MatvecArgs a,
             for (int e = 0; e < SUMS; ++e) lds.sums[wave][(i * NB + j) * 4 + e][lane] = acc[i][j][e];
     __syncthreads();
 
-    store_sums<F, GROUP, MB, NB>(a, XT, yt, m0, n0, rows_m, rows_n, waves, &lds.sums[0], kUnit<HALF, F>,
+    store_sums<F, GROUP, MB, NB>(a, XT, yt, m0, n0, rows_m, rows_n, waves, &lds.sums[0], kUnit<XT, F>,
                                 XT == X::F8_ROW ? static_cast<const float*>(a.xscales) : nullptr);
 }
 

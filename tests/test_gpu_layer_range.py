@@ -80,3 +80,68 @@ KINDS = ["bf16", "f16", "f8block", "f8row"]
 def test_a_large_column_without_weight_leaves_the_others(kind, fmt, group, zeros):
     """Up to 16 rows of x: a column whose weights are zero adds nothing, however large it is."""
     check_large_column(kind, fmt, group, zeros, (1, 4, 7, 16))
+
+
+def check_scale_bytes(rows):
+    """Every kind of scale byte of 8-bit x against 4-bit float weights of every kind of scale: exact where the result
+    is a normal number, infinite or NaN where it is."""
+    import torch
+    import dense_linear_algebra_potrf_amd as bl
+    xb = np.array([0, 1, 2, 3, 4, 5, 60, 120, 127, 200, 243, 244, 246, 247, 251, 252, 253, 254, 255], np.uint8)
+    wb = np.array([0, 1, 2, 60, 127, 131, 200, 240, 252, 253, 254], np.uint8)
+    rng = np.random.default_rng(0)
+    small = np.concatenate([np.arange(0, 0x39), np.arange(0x80, 0xb9)])         # e4m3 values up to 1, subnormal ones among them
+    for m in rows:
+        for k in (20, 100, 300):
+            blocks = -(-k // 32)
+            x = torch.from_numpy(rng.choice(small, (m, k)).astype(np.uint8)).view(torch.float8_e4m3fn)
+            if m > 1:
+                x[0] = 0                                                        # an empty row, whatever its scales are
+            codes = rng.integers(0, 16, (len(wb), k))
+            b = np.broadcast_to(wb[:, None], (len(wb), blocks)).copy()
+            held = ref.held(codes, 2.0 ** (b.astype(np.float64) - 127), None, "fp4", 32, k)
+            cc, cs = torch.from_numpy(ref.pack(codes)).cuda(), torch.from_numpy(b).view(torch.float8_e8m0fnu).cuda()
+            for shift in range(0, len(xb), m):
+                announce("weight_matvec scale bytes", m, k, shift)
+                s = np.broadcast_to(xb[(np.arange(m) + shift) % len(xb)][:, None], (m, blocks)).copy()
+                with np.errstate(all="ignore"):
+                    one = np.where(s[:, 0] == 255, np.nan, 2.0 ** (s[:, 0].astype(np.float64) - 127))
+                    want = ((ref.f64(x.float()) * one[:, None]) @ held.T).astype(np.float32)
+                y = bl.weight_matvec(x.cuda(), cc, cs, format="fp4", x_scales=torch.from_numpy(s).view(torch.float8_e8m0fnu).cuda(),
+                                     out_dtype=torch.float32).cpu().numpy()
+                assert np.array_equal(np.isnan(y), np.isnan(want))
+                inf = np.isinf(want)
+                assert np.array_equal(y[inf], want[inf])
+                with np.errstate(all="ignore"):
+                    # subnormal results: each group rounds to a step
+                    ok = np.abs(y - want) <= np.where(np.abs(want) < 2.0 ** -126, (blocks + 1) * SUBNORMAL["f32"], 0)
+                ok |= ~np.isfinite(want)
+                assert ok.all(), [(int(s[i, 0]), int(wb[j]), float(y[i, j]), float(want[i, j])) for i, j in np.argwhere(~ok)[:6]]
+
+
+@pytest.mark.parametrize("m", [1, 4, 7, 16])
+def test_scale_bytes_of_a_few_rows(m):
+    check_scale_bytes((m,))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("m", [1, 4, 16, 17, 33])
+def test_subnormal_x(kind, m):
+    """The smallest numbers of x's type, times large weights: exact."""
+    import torch
+    import dense_linear_algebra_potrf_amd as bl
+    announce("weight_matvec subnormal x", kind, m)
+    n, k = 20, 200
+    step = 2.0 ** (-133 if kind == "bf16" else -24)
+    x = (torch.randint(-8, 9, (m, k), generator=torch.Generator().manual_seed(m)).double() * step).to(dtypes()[kind])
+    assert np.array_equal(ref.f64(x) / step, np.rint(ref.f64(x) / step)) and x.bool().any()
+    codes = np.random.default_rng(m).integers(0, 16, (n, k))
+    packed = torch.from_numpy(ref.pack(codes)).cuda()
+    b = np.full((n, 7), 220, np.uint8)
+    want = ref.f64(x) @ ref.held(codes, 2.0 ** (b.astype(np.float64) - 127), None, "fp4", 32, k).T
+    y = bl.weight_matvec(x.cuda(), packed, torch.from_numpy(b).view(torch.float8_e8m0fnu).cuda(), format="fp4", out_dtype=torch.float32)
+    assert np.array_equal(ref.f64(y), want)
+    s = torch.full((n, 2), 2.0 ** 90, dtype=torch.bfloat16)
+    want = ref.f64(x) @ ref.held(codes, ref.f64(s), None, "int4", 128, k).T
+    y = bl.weight_matvec(x.cuda(), packed, s.cuda(), out_dtype=torch.float32)
+    assert np.array_equal(ref.f64(y), want)
