@@ -8,13 +8,11 @@
 // lane, the columns in the order in which integer codes come apart, rows and
 // columns past the end zero.
 //
-// On that occasion x becomes half precision, so that the zero point can be
-// subtracted from the codes (packed, exact) and the sums need no correction:
-// bfloat16 and e4m3 values with block scales, times a power of two per row that
-// brings the row's largest below 2^15.  That is exact for everything down to 2^-29
-// of the row's largest (their 8 and 4 significant bits fit in 11) and off by at
-// most 2^-40 of it below, far under the rounding of the 32-bit sums; the power is
-// taken off the results.
+// x keeps the type that a few rows are multiplied in (e4m3 values become 16-bit
+// floats on that occasion), so every value of it goes into the product as it is.  In
+// half precision for all kinds, with a power of two per row, the codes would come
+// apart more cheaply, but what is far below the row's largest value would be lost, and
+// it counts where that value has no weight.
 //
 // What bounds it is the work in the compute unit: for 64 x 8192 x 8192 in groups of
 // 32 (25 us, of it 4.8 for the layout of x) the vector units are busy for 9.5 us
@@ -44,99 +42,30 @@ __device__ __forceinline__ uint64_t load_octet(const uint8_t* p, int left) {
     return e;
 }
 
-// Eight columns of a row of x; those past its end are zero.
-template <X XT>
-struct Octet {
+// Lays out x.  A workgroup takes 16 rows and a chunk's 128 columns, a wavefront 32 of
+// them, a lane 16 bytes of the result: 8 columns of row lane % 16.  2.0 to 4.4 us for
+// 64 x 8192 in a launch of its own, which is latency: 2 MB in and out would take 0.4.
+constexpr int kPackThreads = 256;
+
+template <X XT, Format F>
+__global__ __launch_bounds__(kPackThreads) void pack_kernel(MatvecArgs a, u32x4* out, float* row_scale, int chunks) {
     using T = std::conditional_t<XT == X::F16, f16, bf16>;
-    std::conditional_t<is_eight(XT), uint64_t, Raw8<T>> raw;
-    float block;                                                // the scale of the block they lie in
-
-    __device__ __forceinline__ void load(const MatvecArgs& a, int64_t row, int64_t k) {
-        const int left = int(a.k - k < 8 ? a.k - k : 8);
-        if constexpr (is_eight(XT)) {
-            raw = load_octet(static_cast<const uint8_t*>(a.x) + row * a.ldx + k, left);
-            block = XT == X::F8_BLOCK ? power_of(static_cast<const uint8_t*>(a.xscales)[row * a.ldxs + k / kScaleBlock]) : 1.0f;
-        } else {
-            raw = load8(static_cast<const T*>(a.x) + row * a.ldx + k, left);
+    const int tile = int(blockIdx.x) / chunks, chunk = int(blockIdx.x) % chunks, lane = threadIdx.x & 63;
+    const int64_t row = tile * 16 + (lane & 15), k = int64_t(chunk) * kChunk + (threadIdx.x >> 6) * 32 + (lane >> 4) * 8;
+    const int left = row >= a.m || a.k <= k ? 0 : a.k - k < 8 ? int(a.k - k) : 8;
+    u32x4 v = {0, 0, 0, 0};
+    if constexpr (is_eight(XT)) {
+        if (left) {
+            const uint64_t raw = load_octet(static_cast<const uint8_t*>(a.x) + row * a.ldx + k, left);
+            const float block = XT == X::F8_BLOCK ? block_power(static_cast<const uint8_t*>(a.xscales)[row * a.ldxs + k / kScaleBlock]) : 1.0f;
+            v = __builtin_bit_cast(u32x4, from_e4m3<in_half(XT)>(uint32_t(raw), uint32_t(raw >> 32), block));
         }
+    } else {
+        v = __builtin_bit_cast(u32x4, load8(static_cast<const T*>(a.x) + row * a.ldx + k, left));
     }
-    template <int J>
-    __device__ __forceinline__ float get() const {
-        if constexpr (is_eight(XT)) return __builtin_amdgcn_cvt_f32_fp8(int(uint32_t(raw >> (32 * (J / 4)))), J % 4) * block;
-        else return raw[J];
-    }
-    // The largest finite magnitude, as bits.
-    __device__ __forceinline__ uint32_t top() const {
-        uint32_t most = 0;
-        static_for<0, 8>([&](auto i) {
-            const uint32_t m = magnitude(get<decltype(i)::value>());
-            most = Max{}(most, m < kInfBits ? m : 0);
-        });
-        return most;
-    }
-    // As halves, times the row's factor.
-    __device__ __forceinline__ u32x4 halves(float factor) const {
-        if constexpr (XT == X::F16) return __builtin_bit_cast(u32x4, raw);
-        f16x8 h;
-        static_for<0, 8>([&](auto i) { h[decltype(i)::value] = f16(get<decltype(i)::value>() * factor); });
-        return __builtin_bit_cast(u32x4, h);
-    }
-};
-
-// A workgroup for a row of x (of whole tiles of 16): its largest finite magnitude,
-// then 8 columns a thread at a time; the first kKept of them (16384 columns) stay in
-// registers, so that such a row is read once.  4.8 us for 64 x 8192 in a launch of
-// its own, which is latency: 2 MB in and out would take 0.4.
-constexpr int kPackThreads = 512, kKept = 4;
-
-template <X XT, bool MIXED>
-__global__ __launch_bounds__(kPackThreads) void pack_kernel(MatvecArgs a, u32x4* out, float* row_scale) {
-    __shared__ uint32_t tops[kPackThreads / 64];
-    const int64_t row = blockIdx.x, octets = (a.k + kChunk - 1) / kChunk * 16;
-    const int64_t mine = row < a.m ? (a.k + 7) / 8 : 0;         // octets that hold columns
-    auto put = [&](int64_t o, u32x4 v) {
-        if constexpr (MIXED) v = mixed<false>(v);
-        // (16 rows, 32 columns), then the lane: row, and which 8 of the columns
-        out[(row / 16 * (octets / 4) + o / 4) * 64 + o % 4 * 16 + row % 16] = v;
-    };
-    Octet<XT> kept[kKept];
-#pragma unroll
-    for (int i = 0; i < kKept; ++i)
-        if (threadIdx.x + i * kPackThreads < mine) kept[i].load(a, row, (threadIdx.x + i * kPackThreads) * 8);
-    float factor = 1, scale = 1;
-    if (XT == X::F8_ROW && row < a.m) scale = static_cast<const float*>(a.xscales)[row];
-    if constexpr (XT == X::BF16 || XT == X::F8_BLOCK) {
-        uint32_t top = 0;
-#pragma unroll
-        for (int i = 0; i < kKept; ++i)
-            if (threadIdx.x + i * kPackThreads < mine) top = Max{}(top, kept[i].top());
-        for (int64_t o = threadIdx.x + kKept * kPackThreads; o < mine; o += kPackThreads) {
-            Octet<XT> v;
-            v.load(a, row, o * 8);
-            top = Max{}(top, v.top());
-        }
-        top = block_reduce<kPackThreads>(top, Max{}, tops);
-        if (top) {
-            const int e = int(top >> 23), up = 141 - e < 126 ? 141 - e : 126;   // largest: 2^14 to 2^15
-            factor = __builtin_bit_cast(float, uint32_t(127 + up) << 23);
-            scale = __builtin_bit_cast(float, uint32_t(127 - up) << 23);
-        }
-    }
-    if (threadIdx.x == 0 && row < a.m) row_scale[row] = scale;
-#pragma unroll
-    for (int i = 0; i < kKept; ++i) {
-        const int64_t o = threadIdx.x + i * kPackThreads;
-        if (o < octets) put(o, o < mine ? kept[i].halves(factor) : u32x4{0, 0, 0, 0});
-    }
-    for (int64_t o = threadIdx.x + kKept * kPackThreads; o < octets; o += kPackThreads) {
-        u32x4 h = {0, 0, 0, 0};
-        if (o < mine) {
-            Octet<XT> v;
-            v.load(a, row, o * 8);
-            h = v.halves(factor);
-        }
-        put(o, h);
-    }
+    out[int64_t(blockIdx.x) * kPackThreads + threadIdx.x] = F == Format::INTEGER ? mixed<false>(v) : v;
+    if (chunk == 0 && threadIdx.x < 16 && row < a.m)
+        row_scale[row] = kUnit<XT, F> * (XT == X::F8_ROW ? static_cast<const float*>(a.xscales)[row] : 1.0f);
 }
 
 // Joins the wavefronts' sums in their order (a lane's four of a tile of 16 x 16:
@@ -189,7 +118,7 @@ __device__ __forceinline__ void store_tiles(const MatvecArgs& a, X xt, Type yt, 
     }
 }
 
-template <Format F, int GROUP, int MT, int NB, int WAVES>
+template <bool HALF, Format F, int GROUP, int MT, int NB, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void weight_many_kernel(MatvecArgs a, const u32x4* packed, const float* row_scale,
                                                                      X xt, Type yt) {
     constexpr int MB = MT / 16, GROUPS = kChunk / GROUP, STEPS = GROUP / 32, TILE = 16 * NB;
@@ -280,9 +209,9 @@ __global__ __launch_bounds__(64 * WAVES) void weight_many_kernel(MatvecArgs a, c
                     const int t = s * STEPS + q;
 #pragma unroll
                     for (int j = 0; j < NB; ++j) {
-                        const Frag w = unpack<true, F>(get_codes(j, t), Zero<true>(zeros[j][s]));
+                        const Frag w = unpack<HALF, F>(get_codes(j, t), Zero<HALF>(zeros[j][s]));
 #pragma unroll
-                        for (int i = 0; i < MB; ++i) part[i][j] = product<true>(x[i][t], w, part[i][j]);
+                        for (int i = 0; i < MB; ++i) part[i][j] = product<HALF>(x[i][t], w, part[i][j]);
                     }
                     // x of the next chunk (of this one again, at the end), in the place of what has
                     // been multiplied; not earlier, or it would be held twice
@@ -320,8 +249,11 @@ inline hipError_t weight_many_t(X xt, Type yt, const MatvecArgs& a, void* worksp
         constexpr int MT = decltype(mt)::value, NB = decltype(nb)::value, WAVES = decltype(waves)::value;
         const dim3 block(uint32_t(64 * (chunks < WAVES ? chunks : WAVES)));
         const dim3 grid(uint32_t((a.n + 16 * NB - 1) / (16 * NB)), uint32_t((a.m + MT - 1) / MT));
-        return launch(weight_many_kernel<F, GROUP, MT, NB, WAVES>, grid, block, 0, s, a, static_cast<const u32x4*>(workspace),
-                      static_cast<const float*>(row_scales(a, workspace)), xt, yt);
+        auto go = [&](auto half) {
+            return launch(weight_many_kernel<decltype(half)::value, F, GROUP, MT, NB, WAVES>, grid, block, 0, s, a,
+                          static_cast<const u32x4*>(workspace), static_cast<const float*>(row_scales(a, workspace)), xt, yt);
+        };
+        return in_half(xt) ? go(std::true_type{}) : go(std::false_type{});
     };
     // 32 rows of W to a workgroup where that leaves one for every compute unit: x is read
     // half as often (64 x 8192 x 8192 in groups of 32 25.2 us, 34.3 with 16; 32 x 28672 x
@@ -343,11 +275,12 @@ inline hipError_t weight_many_t(X xt, Type yt, const MatvecArgs& a, void* worksp
 
 template <X XT>
 inline hipError_t pack_t(Format f, const MatvecArgs& a, void* workspace, hipStream_t s) {
-    const dim3 grid(uint32_t((a.m + 15) / 16 * 16));
+    const int64_t chunks = (a.k + kChunk - 1) / kChunk;
+    const dim3 grid(uint32_t((a.m + 15) / 16 * chunks));
     u32x4* out = static_cast<u32x4*>(workspace);
     float* scales = row_scales(a, workspace);
-    return f == Format::INTEGER ? launch(pack_kernel<XT, true>, grid, dim3(kPackThreads), 0, s, a, out, scales)
-                                : launch(pack_kernel<XT, false>, grid, dim3(kPackThreads), 0, s, a, out, scales);
+    return f == Format::INTEGER ? launch(pack_kernel<XT, Format::INTEGER>, grid, dim3(kPackThreads), 0, s, a, out, scales, int(chunks))
+                                : launch(pack_kernel<XT, Format::FLOAT>, grid, dim3(kPackThreads), 0, s, a, out, scales, int(chunks));
 }
 
 }  // namespace weight_matvec_detail

@@ -82,6 +82,13 @@ def test_a_large_column_without_weight_leaves_the_others(kind, fmt, group, zeros
     check_large_column(kind, fmt, group, zeros, (1, 4, 7, 16))
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("fmt,group,zeros", FORMS)
+def test_a_large_column_without_weight_among_many_rows(kind, fmt, group, zeros):
+    """As above from 17 rows of x on."""
+    check_large_column(kind, fmt, group, zeros, (17, 33, 65))
+
+
 def check_scale_bytes(rows):
     """Every kind of scale byte of 8-bit x against 4-bit float weights of every kind of scale: exact where the result
     is a normal number, infinite or NaN where it is."""
@@ -121,6 +128,11 @@ def check_scale_bytes(rows):
 
 @pytest.mark.parametrize("m", [1, 4, 7, 16])
 def test_scale_bytes_of_a_few_rows(m):
+    check_scale_bytes((m,))
+
+
+@pytest.mark.parametrize("m", [17, 40])
+def test_scale_bytes_of_many_rows(m):
     check_scale_bytes((m,))
 
 
