@@ -157,3 +157,45 @@ def test_subnormal_x(kind, m):
     want = ref.f64(x) @ ref.held(codes, ref.f64(s), None, "int4", 128, k).T
     y = bl.weight_matvec(x.cuda(), packed, s.cuda(), out_dtype=torch.float32)
     assert np.array_equal(ref.f64(y), want)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("fmt,group,zeros", FORMS)
+def test_many_rows_on_a_wide_weight(kind, fmt, group, zeros):
+    """More than 32 rows of x on 16384 rows of W and more, which has workgroups of its own: exact, as small integers
+    times small powers of two are; rows shorter than, as long as and longer than one round of the wavefronts."""
+    import torch
+    import dense_linear_algebra_potrf_amd as bl
+    from tests.test_gpu_layer import make_x
+    for i, (m, n, k) in enumerate([(33, 16384, 300), (64, 16401, 512), (65, 16385, 129), (40, 16400, 1500)]):
+        announce("weight_matvec wide and many", kind, fmt, group, zeros, m, n, k)
+        codes, sc, z, cuda = make_weights(i, n, k, fmt, group, zeros, exact=True)
+        x64, x, xs = make_x(i + 40, m, k, kind, exact=True)
+        if kind in ("bf16", "f16") and i == 0:
+            x[7, 3], x[32, 299] = float("inf"), float("nan")
+        with np.errstate(all="ignore"):
+            W = ref.held(codes, sc, z, fmt, group, k)
+            want = x64 @ W.T
+            if kind in ("bf16", "f16") and i == 0:
+                want[7] = (ref.f64(x[7]) * W).sum(1)
+                want[32] = np.nan
+        got = ref.f64(bl.weight_matvec(x, *cuda, format=fmt, group=group, x_scales=xs, out_dtype=torch.float32))
+        assert np.array_equal(got, want, equal_nan=True), f"{int((got != want).sum())} of {want.size} differ"
+
+
+@pytest.mark.parametrize("kind,fmt,group,zeros", [("bf16", "int4", 32, True), ("f8block", "fp4", 32, False), ("f16", "int4", 32, False)])
+def test_many_rows_on_a_wide_weight_with_long_rows(kind, fmt, group, zeros):
+    """As above with more groups to a row than are held at a time."""
+    import torch
+    import dense_linear_algebra_potrf_amd as bl
+    from tests.test_gpu_layer import make_x
+    m, n, k = 34, 16387, 256 * group + 33
+    announce("weight_matvec wide, many and long", kind, fmt, group, zeros, m, n, k)
+    codes, sc, z, cuda = make_weights(1, n, k, fmt, group, zeros, exact=True)
+    x64, x, xs = make_x(2, m, k, kind, exact=True)
+    y = bl.weight_matvec(x, *cuda, format=fmt, group=group, x_scales=xs, out_dtype=torch.float32)
+    got = ref.f64(y)
+    for at in range(0, n, 2048):                    # a part of W at a time in 64 bits
+        rows = slice(at, at + 2048)
+        W = ref.held(codes[rows], sc[rows], None if z is None else z[rows], fmt, group, k)
+        assert np.array_equal(got[:, rows], x64 @ W.T)
