@@ -4,6 +4,10 @@ entry points.  Tensors here are row-major, [rows, columns], with any row stride.
 
 Every operator runs on the current stream, or on `stream`, and tensors that it
 allocates (outputs, workspaces) belong to the stream that it runs on.
+
+Nothing is recorded for automatic differentiation.  rmsnorm_quant and
+weight_matvec refuse floating tensors whose gradient or tangent would be lost;
+the norm's gradient is rmsnorm_grad, and a rounding has none.
 """
 from __future__ import annotations
 
@@ -11,6 +15,7 @@ import ctypes
 import functools
 
 import torch
+from torch.autograd import forward_ad
 
 _TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2, torch.float8_e4m3fn: 3}
 _FORMATS = {"int4": 0, "fp4": 1}
@@ -90,6 +95,17 @@ def _float_type(t, name: str) -> int:
     return code
 
 
+def _refuse_gradients(*tensors):
+    """Refuses tensors whose gradient, or tangent, the call would lose."""
+    for t in tensors:
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            raise ValueError("the gradient would be lost: detach the tensors, or call under torch.no_grad()")
+    if forward_ad._current_level >= 0:
+        for t in tensors:
+            if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+                raise ValueError("the tangent would be lost, as a gradient would: pass the primal tensors")
+
+
 def rmsnorm_quant(x, weight, residual=None, *, eps: float = 1e-6, scale: str = "block", out=None,
                   scales=None, residual_out=None, stream=None):
     """Root-mean-square norm of h = x + residual with an output in 8 bits.
@@ -104,6 +120,9 @@ def rmsnorm_quant(x, weight, residual=None, *, eps: float = 1e-6, scale: str = "
                    scales=scales, residual_out=residual_out)
     lib = _lib or _bind()
     ty = _float_type(x, "x")
+    if x.requires_grad or weight.requires_grad or (residual is not None and residual.requires_grad) \
+            or forward_ad._current_level >= 0:
+        _refuse_gradients(x, weight, residual)
     at = _gpu(x)
     rows, n, ldx = _rows(x, "x")
     dt = x.dtype
@@ -284,6 +303,9 @@ def weight_matvec(x, codes, scales, zeros=None, *, format: str = "int4", group: 
     xt = _TYPES.get(x.dtype, -1)
     if xt < 1:
         raise TypeError(f"x must be bfloat16, float16 or float8_e4m3fn, not {x.dtype}")
+    if x.requires_grad or scales.requires_grad or (x_scales is not None and x_scales.requires_grad) \
+            or forward_ad._current_level >= 0:
+        _refuse_gradients(x, scales, x_scales)
     at = _gpu(x)
     m, k, ldx = _rows(x, "x")
     st_type = _scale_type(format)
