@@ -10,9 +10,9 @@
 // magnitude takes two quad permutes.
 //
 // HBM bounds it: 2 + 2 + 2 + 1 bytes an element in 16 bits with a residual.
-// 8192 x 8192 bf16, residual, block scales: 97 us, 4.9 TB/s where a large copy
-// reaches 5.1.  A single row of 4096 takes 7.3 us a call, of which the kernel
-// is less than the launch.  Loading a row ahead in a grid of 1280 workgroups
+// 8192 x 8192 bf16, residual, block scales: 97 us in calls back to back, 97 to 107
+// (102 on average, 4.6 TB/s) in a profile; a large copy reaches 5.1.  A single row of
+// 4096 takes 7.7 us a call, of which the kernel, 3.6, is less than the launch.  Loading a row ahead in a grid of 1280 workgroups
 // took 102 us at that size (registers for half as many wavefronts), 3 to 7%
 // less below 1024 columns: not done.
 #pragma once
@@ -154,8 +154,8 @@ __global__ __launch_bounds__(Shape<TPR>::threads) void rmsnorm_quant_kernel(Norm
 //
 // HBM bounds it (four rows of 16 bits an element in and out with dh).  With
 // only 512 workgroups to hide it, the latency of a row's load showed: 8192 x
-// 4096 bf16 took 80 us, and 52 (5.1 TB/s) with the next row on its way while
-// this one is reduced and stored.  Where two rows and a sum do not fit the
+// 4096 bf16 took 80 us a call, and 55.5 with the next row on its way while this one
+// is reduced and stored (in a profile 50.9, 5.3 TB/s, and 5.0 for the sum of dw).  Where two rows and a sum do not fit the
 // registers (more than 8 bytes a column and thread) it loads in order.
 template <typename T, int TPR, int VPT>
 __global__ __launch_bounds__(Shape<TPR>::threads) void rmsnorm_grad_kernel(NormGradArgs a, float* dw) {
@@ -292,7 +292,7 @@ __global__ __launch_bounds__(Shape<TPR>::threads) void rmsnorm_grad_kernel(NormG
 
 // dw[c] = the sum of `count` rows of partial sums: 32 columns and 8 slices of
 // the rows per workgroup, the slices joined in LDS.  Bound by latency: 512 rows
-// of 4096 take 4 us with eight loads of a slice on their way at a time; one at
+// of 4096 take 4 to 5 us with eight loads of a slice on their way at a time; one at
 // a time cost 517 x 1537 f32 two of its 16 us.
 static __global__ __launch_bounds__(256) void rmsnorm_dw_kernel(const float* partial, int64_t count, int n, float* dw) {
     __shared__ float slice[8][33];

@@ -14,14 +14,14 @@
 // apart more cheaply, but what is far below the row's largest value would be lost, and
 // it counts where that value has no weight.
 //
-// What bounds it is the work in the compute unit: for 64 x 8192 x 8192 in groups of
-// 32 (25 us, of it 4.8 for the layout of x) the vector units are busy for 9.5 us
-// (scaling the sums 3.4, unpacking 2.3, the rest mostly before and after the loop),
-// the matrix cores for 3.4, and 1 MB of x goes from the L2 to each compute unit, 20
-// TB/s in all; the codes alone would take 7.  Groups of 128 take 22.5 us, 32 rows of
-// x 17.4.  Scaling the last group and unpacking the next one while a product runs
-// gained nothing (24.8), nor did codes from the cache (24.3): the two wavefronts of
-// a SIMD already overlap.
+// What bounds it is the work in the compute unit: for 64 x 8192 x 8192 bfloat16 in
+// groups of 32 (23.3 us a call; in a profile 21.9 and 4.9 for the layout of x) the
+// vector units are busy for 10.7 us (unpacking 4.1, scaling the sums 3.4, the rest
+// mostly before and after the loop), the matrix cores for 3.4, and 1 MB of x goes from
+// the L2 to each compute unit, 12 TB/s in all; the codes alone would take 7.  Groups of
+// 128 take 21.4 us, 32 rows of x 18.0.  When it took 24.9, scaling the last group and
+// unpacking the next one while a product runs gained nothing (24.8), nor did codes from
+// the cache (24.3): the two wavefronts of a SIMD already overlap.
 #pragma once
 
 #include "weight_matvec_impl.hpp"
@@ -43,7 +43,7 @@ __device__ __forceinline__ uint64_t load_octet(const uint8_t* p, int left) {
 }
 
 // Lays out x.  A workgroup takes 16 rows and a chunk's 128 columns, a wavefront 32 of
-// them, a lane 16 bytes of the result: 8 columns of row lane % 16.  2.0 to 4.4 us for
+// them, a lane 16 bytes of the result: 8 columns of row lane % 16.  2.0 to 4.9 us for
 // 64 x 8192 in a launch of its own, which is latency: 2 MB in and out would take 0.4.
 constexpr int kPackThreads = 256;
 
@@ -72,7 +72,7 @@ __global__ __launch_bounds__(kPackThreads) void pack_kernel(MatvecArgs a, u32x4*
 // rows 4 (lane / 16) .. + 3 of x, column lane % 16), times the scale of x's row, and
 // stores y.  A wavefront takes a tile, with 16-byte reads; element by element, with
 // the row's scale from memory, 64 x 28672 x 8192 in groups of 128 took 76.9 us
-// instead of 72.9, and 64 x 28672 x 512 20.0 instead of 15.4.
+// instead of 72.9 (72.3 now), and 64 x 28672 x 512 20.0 instead of 15.4 (15.0 now).
 template <Format F, int GROUP, int MB, int NB, int WAVES>
 __device__ __forceinline__ void store_tiles(const MatvecArgs& a, X xt, Type yt, int64_t m0, int64_t n0, int rows_m, int rows_n,
                                             int waves, const f32x4 (*sums)[MB * NB][64], const float* row_scale) {
@@ -256,14 +256,14 @@ inline hipError_t weight_many_t(X xt, Type yt, const MatvecArgs& a, void* worksp
         return in_half(xt) ? go(std::true_type{}) : go(std::false_type{});
     };
     // 32 rows of W to a workgroup where that leaves one for every compute unit: x is read
-    // half as often (64 x 8192 x 8192 in groups of 32 25.2 us, 34.3 with 16; 32 x 28672 x
-    // 8192 53.8 and 68.8).  With 64 rows of x a compute unit has the registers and LDS of
+    // half as often (64 x 8192 x 8192 in groups of 32 23.6 us, 33.4 with 16; 32 x 28672 x
+    // 8192 52.7 and 68.0).  With 64 rows of x a compute unit has the registers and LDS of
     // one workgroup of 8 wavefronts, and waits while it starts and joins: two of 4 where
-    // there are so many (64 x 28672 x 8192 76.9 us, 84.3 with 8; 64 x 16384 x 4096 23.2 and
-    // 26.1; 64 x 28672 x 512 20.0 and 35.0).  32 rows of x leave room for several (32 x 16384
-    // x 8192 26.1 us, 29.0 with 4).
-    // 32 rows of x where there are no more (17 x 8192 x 8192 16.7 us, 19.3 as 64; 32 x 28672
-    // x 8192 53.8 and 69.5).
+    // there are so many (64 x 28672 x 8192 72.3 us, 81.1 with 8; 64 x 16384 x 4096 20.8 and
+    // 23.5; 64 x 28672 x 512 15.0 and 23.2).  32 rows of x leave room for several (32 x 16384
+    // x 8192 in groups of 32 26.7 us, 32.3 with 4; 32 x 28672 x 8192 52.7 and 52.0).
+    // 32 rows of x where there are no more (17 x 8192 x 8192 16.0 us, 19.8 as 64; 32 x 28672
+    // x 8192 52.7 and 59.9).
     auto rows = [&](auto mt) {
         if constexpr (decltype(mt)::value == 64)
             if (a.n >= 512 * 32) return tile(mt, ic<2>{}, ic<4>{});

@@ -6,11 +6,11 @@
 // which is why even one row goes over the matrix cores: on the vector units, with a
 // conversion, a scale and a multiplication per code and row, 1 x 28672 x 8192 took
 // 412 us.  Measured, with what a copy of those bytes would take:
-//     1 x 28672 x 8192, half precision, groups of 64, zero points  29.0 us (25.2)
-//     1 x 16384 x 8192, bfloat16, groups of 128                    13.6    (13.6)
-//     4 x 16384 x 4096, e4m3 blocks, e2m1 weights                   9.6    (7.0)
-//     16 x 8192 x 8192, bfloat16, groups of 128                    11.0    (6.9)
-//     1 x 4096 x 4096: 4.2 us in the kernel, 7.2 a call
+//     1 x 28672 x 8192, half precision, groups of 64, zero points  29.4 us (25.2)
+//     1 x 16384 x 8192, bfloat16, groups of 128                    16.5    (13.6)
+//     4 x 16384 x 4096, e4m3 blocks, e2m1 weights                   9.1    (7.0)
+//     16 x 8192 x 8192, bfloat16, groups of 128                    12.5    (6.9)
+//     1 x 4096 x 4096: 5.0 to 5.4 us in the kernel, 7.2 a call
 //
 // A wavefront multiplies 16 MB rows of x with 16 NB rows of W over chunks of
 // 128 columns; the wavefronts of a workgroup take every WAVES-th chunk and join
@@ -25,12 +25,14 @@
 // packed in half precision, for bfloat16 (which has no packed sums) by an fma from
 // half precision to 32 bits each.  All of it is exact, so the zero point is off
 // before the product.  Taken off the sums instead (z times the sum of x) it costs
-// less, but a large x whose weight is zero then stands in both sums and takes the
-// bits of the others with it.  Scales are applied to the sums in 32 bits.
+// less (1 x 16384 x 8192 13.6 us in bfloat16, 16.5 as here; 13.6 and 13.9 in half
+// precision), but a large x whose weight is zero then stands in both sums and takes
+// the bits of the others with it.  Scales are applied to the sums in 32 bits.
 //
 // The codes go without their scale, so a sum may leave the range of 32 bits where
 // the definition's does not.  What is not finite is computed again from the
-// definition in 64 bits.
+// definition in 64 bits, an element at a time: one NaN in x takes 1 x 28672 x 8192
+// from 29 us to 1.7 ms, one in 64 rows 64 x 8192 x 8192 from 23 us to 0.5 ms.
 #pragma once
 
 #include "layer_impl.hpp"
@@ -347,11 +349,11 @@ __global__ __launch_bounds__(64 * WAVES) void weight_matvec_kernel(MatvecArgs a,
 
     // Loads a chunk that lies inside the row.  Codes: lane / 4 is the row, lane % 4
     // the 16 bytes of it, so that a load takes whole lines; the transposition to the
-    // matrix cores' layout goes through LDS (16 x 8192 x 8192: 11 us, 14 with loads in
+    // matrix cores' layout goes through LDS (16 x 8192 x 8192 took 11 us then, 14 with loads in
     // that layout and the swaps of lanes).  x: 64 / PER rows a load, PER lanes a row.
     // Rows past the end are not read: their results are not stored.  One chunk ahead:
-    // two and four took 9.0 and 9.5 us for 1 x 16384 x 4096, one 8.0 (the wavefronts
-    // of a compute unit are enough loads on their way, and registers fewer).
+    // two and four took 9.0 and 9.5 us for 1 x 16384 x 4096 when one took 8.0 (the
+    // wavefronts of a compute unit are enough loads on their way, and registers fewer).
     constexpr int PER = ROW / 16, STEP = 64 / PER;
     const uint32_t code_at = uint32_t(lane >> 2) * uint32_t(a.ldc) + 16 * (lane & 3);
     const uint32_t x_at = uint32_t(lane / PER) * uint32_t(a.ldx * ES) + 16 * (lane % PER);
@@ -561,9 +563,9 @@ inline hipError_t weight_matvec_t(Type yt, Format f, int group, const MatvecArgs
     constexpr int FEW = is_eight(XT) ? 8 : 4;                   // rows that one load holds
     auto shape = [&](auto fmt, auto size) {
         // 32 rows of W to a workgroup where that leaves one for every compute unit, since x
-        // and its fragments then serve twice (16 x 8192 x 8192 11.0 us, 13.4 with 16; 1 x
-        // 28672 x 8192 29.0 and 32.5).  Where 16 rows leave one workgroup or none for a
-        // compute unit, its wavefronts are twice as many (4 x 4096 x 14336 9.5 us, 10.8
+        // and its fragments then serve twice (16 x 8192 x 8192 12.5 us, 13.8 with 16; 1 x
+        // 28672 x 8192 30.0 and 32.5).  Where 16 rows leave one workgroup or none for a
+        // compute unit, its wavefronts are twice as many (4 x 4096 x 14336 10.0 us, 11.7
         // with 8; at 4096 columns the call's overhead hides both).
         const bool wide = a.n >= 256 * 32;
         auto rows = [&](auto mt) {
@@ -572,8 +574,8 @@ inline hipError_t weight_matvec_t(Type yt, Format f, int group, const MatvecArgs
             return tile(fmt, size, mt, ic<1>{}, ic<8>{});
         };
         // The matrix cores take 16 rows of x in any case; loading, holding and joining
-        // those that are there: 1 x 28672 x 8192 29.0 us (29.9 as 4 rows, 31.8 as 16), 4 x
-        // 4096 x 14336 9.5 (11.1 as 16).
+        // those that are there: 1 x 28672 x 8192 29.1 us (30.2 as 4 rows, 31.8 as 16), 4 x
+        // 4096 x 14336 10.0 (12.2 as 16).
         return a.m == 1 ? rows(ic<1>{}) : a.m <= FEW ? rows(ic<FEW>{}) : rows(ic<16>{});
     };
     if (f == Format::FLOAT) return shape(std::integral_constant<Format, Format::FLOAT>{}, ic<32>{});

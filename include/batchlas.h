@@ -320,9 +320,11 @@ batchlas_status batchlas_weight_quant(batchlas_type type, batchlas_format format
 /*
  * weight_matvec: y = x W^T, y (m x n), x (m x k), W (n x k) held as codes, sums
  * in 32 bits.  Made for the few rows of a decoding step (m up to about 64);
- * any m up to 2^21 is computed, reading W once per 64 rows.  Where a sum of
- * codes times x leaves the range of 32 bits, the element is computed again in
- * 64 bits, so that y is finite, infinite or NaN as the definition has it.
+ * any m up to 2^21 is computed, reading W once per 64 rows.  x and the codes
+ * less their zero points go into the products exactly, so the error follows
+ * sum |x| |W|.  Where a sum of codes times x leaves the range of 32 bits, the
+ * element is computed again in 64 bits (much more slowly), so that y is
+ * finite, infinite or NaN as the definition has it.
  *   xtype, xscale   F16 or BF16 with NONE, or E4M3 with ROW (xscales float[m])
  *            or BLOCK (bytes, row stride ldxs >= (k + 31) / 32)
  *   ytype    F32, F16 or BF16
