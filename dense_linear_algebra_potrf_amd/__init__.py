@@ -1,5 +1,6 @@
 """Python binding for libbatchlas (batched Cholesky potrf / posv on MI355X, and
-the low-bit layer operators that such solves calibrate, in layer.py).
+the layer operators that such solves calibrate: with 4-bit weights in layer.py,
+with 8-bit integers in integer.py).
 
 Argument marshalling only: every step of the computation runs in the HIP
 kernels of libbatchlas.so, called through its C ABI (include/batchlas.h).
@@ -35,6 +36,8 @@ EXPORTS = [
     "batchlas_route", "batchlas_status_string", "batchlas_last_error", "batchlas_version",
     "batchlas_rmsnorm_quant", "batchlas_rmsnorm_grad", "batchlas_rmsnorm_grad_workspace",
     "batchlas_weight_quant", "batchlas_weight_matvec", "batchlas_weight_matvec_workspace",
+    "batchlas_integer_quant", "batchlas_integer_matmul", "batchlas_block_norm",
+    "batchlas_block_norm_grad", "batchlas_block_norm_grad_workspace",
 ]
 
 
@@ -101,11 +104,21 @@ def load_library():
         lib.batchlas_weight_matvec.argtypes = [i32, i32, i32, i32, i64, i64, i64, i64, vp, i64, vp, i64,
                                                vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp]
         lib.batchlas_weight_matvec_workspace.argtypes = [i64, i64, ctypes.POINTER(i64)]
+        lib.batchlas_integer_quant.argtypes = [i32, i64, i64, vp, i64, vp, vp, i64, vp, vp, i64, vp]
+        lib.batchlas_integer_matmul.argtypes = [i32, i64, i64, i64, vp, i64, vp, vp, i64, vp, vp, i64, vp]
+        lib.batchlas_block_norm.argtypes = [i32, i32, i64, i64, vp, i64, vp, i64, vp, vp, vp, i64, i64,
+                                            f64, f64, vp, i64, vp, i64, vp, vp]
+        lib.batchlas_block_norm_grad.argtypes = [i32, i64, i64, vp, i64, vp, i64, vp, i64, vp, vp, vp,
+                                                 i64, i64, vp, i64, f64, f64, vp, i64, vp, i64, i32,
+                                                 vp, i64, vp, vp, vp, i64, vp]
+        lib.batchlas_block_norm_grad_workspace.argtypes = [i32, i64, i64, i64, ctypes.POINTER(i64)]
         for name in ("batchlas_potrf", "batchlas_posv", "batchlas_potrf_family",
                      "batchlas_posv_family", "batchlas_route", "batchlas_rmsnorm_quant",
                      "batchlas_rmsnorm_grad", "batchlas_rmsnorm_grad_workspace",
                      "batchlas_weight_quant", "batchlas_weight_matvec",
-                     "batchlas_weight_matvec_workspace"):
+                     "batchlas_weight_matvec_workspace", "batchlas_integer_quant",
+                     "batchlas_integer_matmul", "batchlas_block_norm", "batchlas_block_norm_grad",
+                     "batchlas_block_norm_grad_workspace"):
             getattr(lib, name).restype = i32
         lib.batchlas_status_string.argtypes = [i32]
         lib.batchlas_status_string.restype = ctypes.c_char_p
@@ -226,10 +239,12 @@ def version() -> int:
     return load_library().batchlas_version()
 
 
-# ---------------------------------------------------------------- low-bit layer operators
+# ---------------------------------------------------------------- layer operators
 # In modules of their own, which import torch; loaded at first use.
 _LAZY = {"rmsnorm_quant": "layer", "rmsnorm_grad": "layer", "rmsnorm_grad_workspace": "layer",
          "weight_quant": "layer", "weight_matvec": "layer", "weight_matvec_workspace": "layer",
+         "int8_quant": "integer", "int8_matmul": "integer", "block_norm": "integer",
+         "block_norm_grad": "integer", "block_norm_grad_workspace": "integer",
          "calibrate_weights": "calibrate", "second_moments": "calibrate"}
 
 

@@ -1,0 +1,68 @@
+// Device helpers shared by the 8-bit-integer layer operators (gfx950).
+#pragma once
+
+#include "integer.hpp"
+#include "layer_impl.hpp"
+
+namespace bl {
+namespace layer {
+
+constexpr float kCodeMax = 127.0f;
+
+// The scale of a row from the bits of its largest magnitude: NaN where that is not finite.
+__device__ __forceinline__ float code_scale(uint32_t top) {
+    return top >= kInfBits ? __builtin_nanf("") : fmaxf(__builtin_bit_cast(float, top) / kCodeMax, kTiny);
+}
+
+// Codes of eight values under a normal positive scale s, rint(v / s) of the exact
+// quotient, within -127..127; and codes as floats, for what they stand for.
+//
+// t = v (1 / s) is within a few ulp of the quotient, so rint(t) is wrong only next to
+// a half.  There the remainder v - q s is exact in 32 bits (it is at most about s / 2
+// and a multiple of half an ulp of s), and twice of it against s says on which side
+// of the half the quotient is; on it, the even code is taken.  t is rounded by adding
+// 3 2^22, which leaves the code in the lowest byte.
+struct Codes {
+    uint32_t word[2];
+};
+__device__ __forceinline__ Codes to_codes(const float (&v)[8], float s, float inverse, float (&q)[8]) {
+    constexpr float kRound = 12582912.0f;
+    float t[8], far = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        t[j] = fminf(fmaxf(v[j] * inverse, -kCodeMax), kCodeMax);
+        q[j] = (t[j] + kRound) - kRound;
+        far = fmaxf(far, fabsf(t[j] - q[j]));
+    }
+    if (far > 0.4999f) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float d = 2 * fmadd(-q[j], s, v[j]);
+            const bool odd = __builtin_bit_cast(uint32_t, q[j] + kRound) & 1;
+            if (fabsf(d) > s || (fabsf(d) == s && odd)) q[j] += d > 0 ? 1.0f : -1.0f;
+            q[j] = fminf(fmaxf(q[j], -kCodeMax), kCodeMax);
+        }
+    }
+    uint32_t b[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) b[j] = __builtin_bit_cast(uint32_t, q[j] + kRound);
+    auto four = [](uint32_t b0, uint32_t b1, uint32_t b2, uint32_t b3) {
+        const uint32_t lo = __builtin_amdgcn_perm(b1, b0, 0x0c0c0400u), hi = __builtin_amdgcn_perm(b3, b2, 0x04000c0cu);
+        return lo | hi;
+    };
+    return Codes{{four(b[0], b[1], b[2], b[3]), four(b[4], b[5], b[6], b[7])}};
+}
+
+// `count` of 8 codes; p is aligned to 8 bytes.
+__device__ __forceinline__ void store_codes(int8_t* p, const Codes& c, int count) {
+    if (count >= 8) {
+        *reinterpret_cast<uint2*>(p) = uint2{c.word[0], c.word[1]};
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < count) p[i] = int8_t(c.word[i / 4] >> (8 * (i % 4)));
+    }
+}
+
+}  // namespace layer
+}  // namespace bl

@@ -346,6 +346,119 @@ batchlas_status batchlas_weight_matvec(batchlas_type xtype, batchlas_scale xscal
 /* Host-only: the workspace that weight_matvec of this size needs, in bytes. */
 batchlas_status batchlas_weight_matvec_workspace(int64_t m, int64_t k, int64_t *bytes);
 
+/*
+ * 8-bit-integer layer operators
+ * -----------------------------
+ * A layer whose weights are 8-bit integers with a scale for each output channel
+ * and whose activations are 8-bit integers with a scale for each token: the
+ * rounding of either, their products, and the norms that stand between two such
+ * layers' blocks, with their gradient.  Layout, memory, errors and streams are
+ * those of the low-bit layer operators.
+ *
+ * Codes are two's complement bytes; a value is its code times its row's scale (a
+ * float).  Rounding gives codes from -127 to 127; the products take -128 too.
+ * Rows of codes are held in whole 16 bytes, which integer_matmul reads (the padding
+ * may hold anything): codes and their leading dimensions are multiples of 16.
+ */
+
+/*
+ * integer_quant: rounds the rows of x to 8-bit integers.  Per row:
+ *   scale = max(max|x| / 127, 2^-126), rounded to a float,
+ *   q = clamp(rint(x / scale), -127, 127), to nearest, ties to even, of the exact
+ *   quotient
+ *   type     F32, F16 or BF16: of x and values
+ *   given    float[rows]: scales to round under, in place of the row's own, and
+ *            `scales` must be NULL (values beyond 127 scales saturate); NULL:
+ *            none, and `scales` receives the rows' own
+ *   values   receives q times the scale, rounded to the type; NULL: not stored
+ * A row with an x that is not finite gets a NaN scale, codes of zero and NaN
+ * values.  Under given scales a NaN gets a code of zero, and a row whose scale is
+ * not a normal positive number gets codes of zero.  Bytes beyond n of a row are
+ * not written.
+ */
+batchlas_status batchlas_integer_quant(batchlas_type type, int64_t rows, int64_t n, const void *x,
+                                    int64_t ldx, const float *given, int8_t *q, int64_t ldq,
+                                    float *scales, void *values, int64_t ldv,
+                                    batchlas_stream_t stream);
+
+/*
+ * integer_matmul: y[i, j] = xscales[i] * wscales[j] * sum_c x[i, c] * w[j, c], x (m x k)
+ * and w (n x k) codes, y (m x n).  Sums are exact in 32-bit integers; their
+ * product with the scales is computed in 32 bits, in 64 where the two scales'
+ * product leaves the normal range of 32, and rounded to the type.
+ *   ytype    F32, F16 or BF16
+ * NOT_SUPPORTED: k of 2^17 and beyond (sums of 32 bits), m or n beyond 2^24, m * n
+ * beyond 2^36, ldx or ldw beyond 2^22.
+ */
+batchlas_status batchlas_integer_matmul(batchlas_type ytype, int64_t m, int64_t n, int64_t k,
+                                     const int8_t *x, int64_t ldx, const float *xscales,
+                                     const int8_t *w, int64_t ldw, const float *wscales, void *y,
+                                     int64_t ldy, batchlas_stream_t stream);
+
+/*
+ * block_norm: from a block's output y and the residual x to the next block's
+ * input, for every row
+ *   u = post * y / sqrt(mean(y^2) + eps)     (u = y where post is NULL)
+ *   h = residual_scale * x + gate * u        (h = residual_scale * x + u where
+ *                                             gate is NULL)
+ *   v = w * h / sqrt(mean(h^2) + eps)
+ * in 32 bits; v comes from h before h is rounded to the type.
+ *   type     F32, F16 or BF16: of y, x, w, post, gate, h and (NONE) v
+ *   scale    NONE: v in the type, and scales must be NULL; ROW: v in codes with
+ *            a scale a row, as integer_quant rounds it (ldv a multiple of 16)
+ *   gate     gates x n; each row of it is that of rows / gates consecutive rows;
+ *            NULL: none, and gates is not read
+ *   gates    divides rows
+ *   h        may be y or x itself (same leading dimension)
+ *   eps      >= 0;  residual_scale finite
+ * A row whose v is not finite gets a NaN scale and codes of zero.  n is at most
+ * 32768, else NOT_SUPPORTED.
+ */
+batchlas_status batchlas_block_norm(batchlas_type type, batchlas_scale scale, int64_t rows,
+                                    int64_t n, const void *y, int64_t ldy, const void *x,
+                                    int64_t ldx, const void *w, const void *post, const void *gate,
+                                    int64_t gates, int64_t ldg, double residual_scale, double eps,
+                                    void *h, int64_t ldh, void *v, int64_t ldv, float *scales,
+                                    batchlas_stream_t stream);
+
+/*
+ * block_norm_grad: the gradient of the above at the stored h.  With
+ * s = 1 / sqrt(mean(h^2) + eps), t = 1 / sqrt(mean(y^2) + eps), dv the gradient of v
+ * and dh the one that reaches h on the residual path,
+ *   a  = dh + s * (dv * w - h * s^2 * mean(dv * w * h))
+ *   dx = residual_scale * a
+ *   b  = a * gate,  dy = t * (b * post - y * t^2 * mean(b * post * y))
+ *   dw = sum over rows of dv * h * s          (float[n])
+ *   dpost = sum over rows of b * y * t        (float[n])
+ *   dgate = sum over the rows of each gate of a * post * y * t   (gates x n)
+ * and without post dy = b, dgate = sum of a * y; without gate b = a.
+ *   dh       NULL: zero
+ *   dgtype   of dgate: F32 or the type
+ *   dw, dpost, dgate   NULL: not computed; dpost needs post, dgate a gate
+ *   dy, dx   may each be dv, y, h or dh itself (same leading dimension)
+ *   workspace  device memory of at least the bytes that
+ *            batchlas_block_norm_grad_workspace gives, aligned to 4 bytes; not
+ *            used (may be NULL) where that is 0
+ * n is at most 16384, else NOT_SUPPORTED.  rows may be 0: dw, dpost and dgate are
+ * set to zero.
+ */
+batchlas_status batchlas_block_norm_grad(batchlas_type type, int64_t rows, int64_t n,
+                                         const void *dv, int64_t lddv, const void *y, int64_t ldy,
+                                         const void *h, int64_t ldh, const void *w,
+                                         const void *post, const void *gate, int64_t gates,
+                                         int64_t ldg, const void *dh, int64_t lddh,
+                                         double residual_scale, double eps, void *dy, int64_t lddy,
+                                         void *dx, int64_t lddx, batchlas_type dgtype, void *dgate,
+                                         int64_t lddg, float *dw, float *dpost, void *workspace,
+                                         int64_t workspace_bytes, batchlas_stream_t stream);
+
+/*
+ * Host-only: the workspace that block_norm_grad of this size needs, in bytes, where
+ * all of dw, dpost and dgate are computed (0 gates: without a gate).
+ */
+batchlas_status batchlas_block_norm_grad_workspace(batchlas_type type, int64_t rows, int64_t n,
+                                                   int64_t gates, int64_t *bytes);
+
 /* Static text for a status code. */
 const char *batchlas_status_string(batchlas_status s);
 
