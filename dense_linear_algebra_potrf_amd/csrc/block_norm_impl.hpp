@@ -7,7 +7,8 @@
 // share it (VPT vectors of 8 elements each, vector i of thread t at column
 // 8 (i TPR + t)) from its loads through both sums of squares to the stores.
 //
-// HBM bounds it: x, y, h and v (and a gate for each row), a pass each.
+// HBM bounds it: x, y, h and v (and a gate for each row), a pass each.  8192 rows of 8192
+// in bf16 take 121 us (a copy of as many bytes 104), with codes 110 (91), of 4096 57 (52).
 #pragma once
 
 #include "integer_impl.hpp"
@@ -63,6 +64,15 @@ __global__ __launch_bounds__(Shape<TPR>::threads) void block_norm_kernel(BlockNo
     const int t = threadIdx.x % TPR;
     const int n = int(a.n);
     const T* w = static_cast<const T*>(a.w);
+    // Where a row is shared by less than a wave, its end is in every wave's way: loads without
+    // a branch take 124 us in place of 154 for 500000 rows of 100 in f16.  In longer rows
+    // the last threads alone take the branch, and 8192 rows of 8192 take 121 us with it, 127 without.
+    auto at = [&](const T* from, int c) {
+        if constexpr (TPR >= 64) return load8(from + c, n - c);
+        Raw8<T> r = fetch(from, c, n);
+        settle(r, c, n);
+        return r;
+    };
     for (int64_t row = int64_t(blockIdx.x) * S::rows + S::slot(); row < a.rows;
          row += int64_t(gridDim.x) * S::rows) {
         const T* x = static_cast<const T*>(a.x) + row * a.ldx;
@@ -72,9 +82,9 @@ __global__ __launch_bounds__(Shape<TPR>::threads) void block_norm_kernel(BlockNo
         Raw8<T> held[VPT];
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int c = 8 * (i * TPR + t), left = n - c;
-            const Raw8<T> yr = load8(y + c, left);
-            held[i] = load8(x + c, left);
+            const int c = 8 * (i * TPR + t);
+            const Raw8<T> yr = at(y, c);
+            held[i] = at(x, c);
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[i][j] = yr[j];
         }
@@ -84,12 +94,12 @@ __global__ __launch_bounds__(Shape<TPR>::threads) void block_norm_kernel(BlockNo
         for (int i = 0; i < VPT; ++i) {
             const int c = 8 * (i * TPR + t), left = n - c;
             if constexpr (POST) {
-                const Raw8<T> p = load8(static_cast<const T*>(a.post) + c, left);
+                const Raw8<T> p = at(static_cast<const T*>(a.post), c);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * ts * p[j];
             }
             if (a.gate) {
-                const Raw8<T> g = load8(gate + c, left);
+                const Raw8<T> g = at(gate, c);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[i][j] = fmadd(v[i][j], g[j], a.c * held[i][j]);
             } else {
@@ -106,7 +116,7 @@ __global__ __launch_bounds__(Shape<TPR>::threads) void block_norm_kernel(BlockNo
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int c = 8 * (i * TPR + t), left = n - c;
-            const Raw8<T> wr = load8(w + c, left);
+            const Raw8<T> wr = at(w, c);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 v[i][j] = v[i][j] * rs * wr[j];
@@ -132,74 +142,96 @@ __global__ __launch_bounds__(Shape<TPR>::threads) void block_norm_kernel(BlockNo
 }
 
 // ---------------------------------------------------------------- gradient
-// With g = dv w, unit vectors h s and y t of the two norms, and the row's gate:
-//     a = dh + s (g - (h s) mean(g h s)),   dx = c a,   b = a gate,
-//     dy = t (b post - (y t) mean(b post y t)),
-//     dw = sum dv (h s),  and S = sum a (y t) over the rows of one gate, from which
+// With e = dv w, the unit rows u = h s and z = y t of the two norms, and the row's gate:
+//     a = dh + s (e - u mean(e u)),   dx = c a,   b = a gate,
+//     dy = t (b post - z mean(b post z)),
+//     dw = sum dv u,  and S = sum a z over the rows of one gate, from which
 //     dgate = post S and dpost = sum over gates of gate S.
-// Without post, y t is y itself, dy = b and dgate = S.
+// Without post, z is y itself, dy = b and dgate = S.
+//
+// With k = gate post y, the last mean comes apart into sums that need neither root nor
+// the other mean, so that a row takes one reduction and one barrier:
+//     sum(b post z) = t (sum(k dh) + s sum(k e) - s^2 mean(e u) sum(k h)).
+// (Three reductions, one after the other, took 130 us where this takes 97.)
 //
 // Each group of TPR threads takes a run of consecutive rows and keeps its sums over
 // them in registers: runs either lie within one gate's rows, whose sums S then go to
 // the workspace, or hold whole gates, whose dgate is then written at each gate's end
-// while gate S goes on in registers.  The workspace's sums are added in a fixed
-// order by block_grad_sums_kernel: no atomics, so two runs agree bit for bit.
+// while gate S goes on in LDS.  The workspace's sums are added in a fixed order by
+// block_grad_sums_kernel: no atomics, so two runs agree bit for bit.
+//
+// HBM bounds it: dv, y, h and dh are read and dx and dy written once.  8192 rows of 4096 in bf16
+// with eight gates take 97 us, 89 of them here and 7 in the sums (a copy of as many
+// bytes 78), in f32 169 (157), 4096 of 8192 in bf16 96 (78).  517 rows of 1537 take
+// 18 us, 11 here and 4 in the sums: the latency of two launches.
 struct Runs {
     int64_t rows;        // of a run
-    int64_t of_gate;     // runs of one gate; 0: a run holds whole gates (or there are none)
+    int64_t of_gate;     // runs of one gate, whole workgroups of them; 0: a run holds whole gates (or there are none)
     int64_t count;
 };
 
-// Sums of three values over THREADS threads with one barrier.
-template <int THREADS>
-__device__ __forceinline__ void reduce3(float& a, float& b, float& c, float (*slot)[3]) {
+// A row's sums: h^2, e h and, with post, y^2, k dh, k e and k h.
+struct RowSums {
+    float h2, eh, y2, kd, ke, kh;
+};
+
+// Their sums over THREADS threads, with one barrier.
+template <int THREADS, bool POST>
+__device__ __forceinline__ RowSums reduce(RowSums v, RowSums* slot) {
     constexpr int LANES = THREADS < 64 ? THREADS : 64;
-    a = wave_reduce<LANES>(a, Add{});
-    b = wave_reduce<LANES>(b, Add{});
-    c = wave_reduce<LANES>(c, Add{});
+    v.h2 = wave_reduce<LANES>(v.h2, Add{});
+    v.eh = wave_reduce<LANES>(v.eh, Add{});
+    if constexpr (POST) {
+        v.y2 = wave_reduce<LANES>(v.y2, Add{});
+        v.kd = wave_reduce<LANES>(v.kd, Add{});
+        v.ke = wave_reduce<LANES>(v.ke, Add{});
+        v.kh = wave_reduce<LANES>(v.kh, Add{});
+    }
     if constexpr (THREADS > 64) {
-        if ((threadIdx.x & 63) == 0) {
-            slot[threadIdx.x >> 6][0] = a;
-            slot[threadIdx.x >> 6][1] = b;
-            slot[threadIdx.x >> 6][2] = c;
-        }
+        if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
         __syncthreads();
-        a = slot[0][0], b = slot[0][1], c = slot[0][2];
+        v = slot[0];
 #pragma unroll
-        for (int i = 1; i < THREADS / 64; ++i) a += slot[i][0], b += slot[i][1], c += slot[i][2];
+        for (int i = 1; i < THREADS / 64; ++i) {
+            const RowSums o = slot[i];
+            v.h2 += o.h2, v.eh += o.eh;
+            if constexpr (POST) v.y2 += o.y2, v.kd += o.kd, v.ke += o.ke, v.kh += o.kh;
+        }
     }
+    return v;
 }
 
-// The next row is on its way while this one is reduced and stored, where the
-// registers have room for two; else y and dh are loaded where they are used.
-template <typename T, int VPT> constexpr bool kAhead = VPT * sizeof(T) <= 4;
-// In the widest shape h and dv are loaded where they are used, too (from the cache).
-template <int VPT> constexpr bool kHold = VPT <= 2;
-// Then the loads of one vector also stay behind the work on the last.
-template <bool AHEAD>
-__device__ __forceinline__ void in_turn() {
-    if constexpr (!AHEAD) {
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_sched_barrier(0);
-    }
-}
+// What a shape's registers have room for: the weights over all rows and the next row
+// while this one is reduced and stored; or only this row; or not even that (it then comes
+// from the cache a second time, which rows beyond 8192 pay with 153 us where a copy takes 78).
+template <typename T, int TPR, int VPT> constexpr bool kAhead = TPR <= 512 && VPT * sizeof(T) <= 4;
+template <typename T, int TPR, int VPT> constexpr bool kHold = TPR <= 512 && VPT <= 2;
 
-// The workspace: dw's sums, a row of n for each workgroup, then either S, a row for
-// each run, or dpost's, a row for each workgroup.
+// The sums hold products of h and y with the gradients, which may be large or small
+// themselves: h and y are scaled sooner than their squares alone would need.
+__device__ __forceinline__ bool near_one(float mean) { return mean > 0x1p-48f && mean < 0x1p48f; }
+
+// The workspace: dw's sums, a row of n for each workgroup, then as many of either S or
+// dpost's.
 template <typename T, int TPR, int VPT, bool POST>
 __global__ __launch_bounds__(Shape<TPR>::threads) void block_grad_kernel(BlockGradArgs a, Runs runs, float* dw, float* second) {
     using S = Shape<TPR>;
-    constexpr bool AHEAD = kAhead<T, VPT>, HOLD = kHold<VPT>;
-    __shared__ float sums[2][S::waves][3], ysums[S::waves];
-    __shared__ uint32_t tops[2][S::waves];
+    constexpr bool AHEAD = kAhead<T, TPR, VPT>, HOLD = kHold<T, TPR, VPT>;
+    // by the row's parity, so that the next row's may be written while this one's are read
+    __shared__ RowSums sums[2][S::waves], again[2][S::waves];
+    __shared__ uint32_t tops[2][2][S::waves];
     const int t = threadIdx.x % TPR;
     const int n = int(a.n);
     const int64_t run = int64_t(blockIdx.x) * S::rows + S::slot();
-    const T* const w = static_cast<const T*>(a.w);
-    const T* const post = static_cast<const T*>(a.post);
+    auto send_for = [&](const void* p, int64_t row, int64_t ld, int i) {
+        int c = 8 * (i * TPR + t);
+        asm volatile("" : "+v"(c));                             // no address is kept from one row to the next
+        return fetch(static_cast<const T*>(p) + row * ld, c, n);
+    };
     auto at = [&](const void* p, int64_t row, int64_t ld, int i) {
-        const int c = 8 * (i * TPR + t);
-        return load8(static_cast<const T*>(p) + row * ld + c, n - c);
+        Raw8<T> r = send_for(p, row, ld, i);
+        settle(r, 8 * (i * TPR + t), n);
+        return r;
     };
     auto put = [&](void* p, int64_t row, int64_t ld, int i, const float (&v)[8]) {
         const int c = 8 * (i * TPR + t);
@@ -208,7 +240,7 @@ __global__ __launch_bounds__(Shape<TPR>::threads) void block_grad_kernel(BlockGr
     // dpost's sum over whole gates is touched once a gate: it lies in LDS, a thread's
     // own slots, for the registers it would take
     __shared__ float psum[VPT][8][S::threads];
-    __shared__ float glds[HOLD ? 1 : VPT][8][HOLD ? 1 : S::threads];    // S too, in the widest shape
+    __shared__ float glds[HOLD ? 1 : VPT][8][HOLD ? 1 : S::threads];    // S too, in the widest shapes
     float wsum[VPT][8], gkept[HOLD ? VPT : 1][8];
     auto gsum = [&](int i, int j) -> float& {
         if constexpr (HOLD) return gkept[i][j];
@@ -228,191 +260,211 @@ __global__ __launch_bounds__(Shape<TPR>::threads) void block_grad_kernel(BlockGr
     if (end > a.rows) end = a.rows;
     int64_t gate_row = a.gate && row < end ? row / a.per : 0;
     int64_t in_gate = a.gate && row < end ? row - gate_row * a.per : 0;
-    Raw8<T> hn[AHEAD ? VPT : 1], vn[AHEAD ? VPT : 1], yn[AHEAD ? VPT : 1], en[AHEAD ? VPT : 1];
-    auto load = [&](int64_t r) {
-        if constexpr (AHEAD) {
+
+    // where registers are short, a vector's loads stay behind the last one's work
+    auto in_turn = [] {
+        if constexpr (!HOLD) __builtin_amdgcn_sched_barrier(0);
+    };
+    // the next row on its way, and this one
+    constexpr int NEXT = AHEAD ? VPT : 1, KEPT = HOLD ? VPT : 1;
+    Raw8<T> hn[NEXT], vn[NEXT], yn[NEXT], dn[NEXT], hk[KEPT], vk[KEPT], yk[KEPT], dk[KEPT], wk[NEXT], pk[NEXT], gk[NEXT];
+    auto load_next = [&](int64_t r) {
+        if constexpr (AHEAD)
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                hn[i] = at(a.h, r, a.ldh, i);
-                vn[i] = at(a.dv, r, a.lddv, i);
-                yn[i] = at(a.y, r, a.ldy, i);
-                if (a.dh) en[i] = at(a.dh, r, a.lddh, i);
+                hn[i] = send_for(a.h, r, a.ldh, i);
+                vn[i] = send_for(a.dv, r, a.lddv, i);
+                yn[i] = send_for(a.y, r, a.ldy, i);
+                if (a.dh) dn[i] = send_for(a.dh, r, a.lddh, i);
             }
-        }
     };
-    if (row < end) load(row);
-    for (; row < end; ++row) {
-        Raw8<T> hkept[HOLD ? VPT : 1], vkept[HOLD ? VPT : 1], ykept[AHEAD ? VPT : 1], ekept[AHEAD ? VPT : 1];
-        float square = 0, dot = 0, ysquare = 0;
+    if (AHEAD && row < end) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            Raw8<T> hr, vr, yr;
-            if constexpr (AHEAD) {
-                hr = hn[i];
-                vr = vn[i];
-                yr = ykept[i] = yn[i];
-                ekept[i] = en[i];
-            } else {
-                hr = at(a.h, row, a.ldh, i);
-                vr = at(a.dv, row, a.lddv, i);
-                if constexpr (POST) yr = at(a.y, row, a.ldy, i);
-            }
-            if constexpr (HOLD) {
-                hkept[i] = hr;
-                vkept[i] = vr;
-            }
-            const Raw8<T> wr = at(w, 0, 0, i);
-            float squares = 0, dots = 0, ysquares = 0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                squares = fmadd(hr[j], hr[j], squares);
-                dots = fmadd(vr[j] * wr[j], hr[j], dots);
-                if constexpr (POST) ysquares = fmadd(yr[j], yr[j], ysquares);
-            }
-            square += squares;
-            dot += dots;
-            ysquare += ysquares;
-            in_turn<AHEAD>();
+            wk[i] = at(a.w, 0, 0, i);
+            if constexpr (POST) pk[i] = at(a.post, 0, 0, i);
+            if (a.gate) gk[i] = at(a.gate, gate_row, a.ldg, i);
         }
-        if (AHEAD && row + 1 < end) load(row + 1);
-        auto keep_packed = [&] {
-#pragma unroll
-            for (int i = 0; i < VPT; ++i) {
-                if constexpr (HOLD) {
-                    hkept[i].keep_packed();
-                    vkept[i].keep_packed();
-                }
-                if constexpr (AHEAD) ykept[i].keep_packed();
-            }
-        };
-        keep_packed();
-        reduce3<TPR>(square, dot, ysquare, sums[0]);
+        load_next(row);
+    }
+    auto w_at = [&](int i) {
+        if constexpr (AHEAD) return wk[i];
+        else return at(a.w, 0, 0, i);
+    };
+    auto p_at = [&](int i) {
+        if constexpr (AHEAD) return pk[i];
+        else return at(a.post, 0, 0, i);
+    };
+    auto g_at = [&](int i) {
+        if constexpr (AHEAD) return gk[i];
+        else return at(a.gate, gate_row, a.ldg, i);
+    };
+    for (int parity = 0; row < end; ++row, parity ^= 1) {
         auto h_at = [&](int i) {
-            if constexpr (HOLD) return hkept[i];
+            if constexpr (HOLD) return hk[i];
             else return at(a.h, row, a.ldh, i);
         };
         auto v_at = [&](int i) {
-            if constexpr (HOLD) return vkept[i];
+            if constexpr (HOLD) return vk[i];
             else return at(a.dv, row, a.lddv, i);
         };
         auto y_at = [&](int i) {
-            if constexpr (AHEAD) return ykept[i];
+            if constexpr (HOLD) return yk[i];
             else return at(a.y, row, a.ldy, i);
         };
-        float mean = square / float(n) + a.eps, f = 1;
-        if (!mean_in_range(mean)) {
-            uint32_t most = 0;
+        auto d_at = [&](int i) {
+            if constexpr (HOLD) return dk[i];
+            else return at(a.dh, row, a.lddh, i);
+        };
+        // sums of h f and y yf in the place of h and y
+        auto sum_up = [&](float f, float yf) {
+            RowSums sum = {0, 0, 0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const Raw8<T> hr = h_at(i), vr = v_at(i), wr = w_at(i);
+                RowSums part = {0, 0, 0, 0, 0, 0};              // short chains: small errors
+                float e[8], h[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    e[j] = vr[j] * wr[j];
+                    h[j] = hr[j] * f;
+                    part.h2 = fmadd(h[j], h[j], part.h2);
+                    part.eh = fmadd(e[j], h[j], part.eh);
+                }
+                in_turn();
+                if constexpr (POST) {
+                    const Raw8<T> yr = y_at(i), pr = p_at(i);
+                    float k[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        k[j] = yr[j] * yf;
+                        part.y2 = fmadd(k[j], k[j], part.y2);
+                        k[j] *= pr[j];
+                    }
+                    in_turn();
+                    if (a.gate) {
+                        const Raw8<T> gr = g_at(i);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) k[j] *= gr[j];
+                    }
+                    in_turn();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        part.ke = fmadd(k[j], e[j], part.ke);
+                        part.kh = fmadd(k[j], h[j], part.kh);
+                    }
+                    if (a.dh) {
+                        const Raw8<T> dr = d_at(i);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) part.kd = fmadd(k[j], dr[j], part.kd);
+                    }
+                }
+                sum.h2 += part.h2, sum.eh += part.eh;
+                if constexpr (POST) sum.y2 += part.y2, sum.kd += part.kd, sum.ke += part.ke, sum.kh += part.kh;
+                in_turn();
+            }
+            return sum;
+        };
+        if constexpr (HOLD) {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                if constexpr (AHEAD) {
+                    hk[i] = hn[i], vk[i] = vn[i], yk[i] = yn[i], dk[i] = dn[i];
+                } else {
+                    hk[i] = send_for(a.h, row, a.ldh, i);
+                    vk[i] = send_for(a.dv, row, a.lddv, i);
+                    yk[i] = send_for(a.y, row, a.ldy, i);
+                    if (a.dh) dk[i] = send_for(a.dh, row, a.lddh, i);
+                }
+            }
+            if (AHEAD && row + 1 < end) load_next(row + 1);
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const int c = 8 * (i * TPR + t);
+                settle(hk[i], c, n), settle(vk[i], c, n), settle(yk[i], c, n);
+                if (a.dh) settle(dk[i], c, n);
+            }
+        }
+        const bool last = !runs.of_gate && a.gate && ++in_gate == a.per;    // of a gate, in a run of whole gates
+        RowSums sum = sum_up(1.0f, 1.0f);
+        auto keep_packed = [&] {
+            if constexpr (HOLD) {
+#pragma unroll
+                for (int i = 0; i < VPT; ++i) {
+                    hk[i].keep_packed(), vk[i].keep_packed(), yk[i].keep_packed(), dk[i].keep_packed();
+                    if constexpr (AHEAD) wk[i].keep_packed(), pk[i].keep_packed(), gk[i].keep_packed();
+                }
+            }
+        };
+        keep_packed();
+        sum = reduce<TPR, POST>(sum, sums[parity]);
+        float f = 1, yf = 1, mean = sum.h2 / float(n) + a.eps, ymean = POST ? sum.y2 / float(n) + a.eps : 1.0f;
+        if (!near_one(mean) || !near_one(ymean)) {
+            uint32_t most = 0, ymost = 0;
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 const Raw8<T> hr = h_at(i);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) most = Max{}(most, magnitude(hr[j]));
-            }
-            f = rescale(block_reduce<TPR>(most, Max{}, tops[0]));
-            square = dot = 0;
-            float none = 0;
+                if constexpr (POST) {
+                    const Raw8<T> yr = y_at(i);
 #pragma unroll
-            for (int i = 0; i < VPT; ++i) {
-                const Raw8<T> wr = at(w, 0, 0, i), hr = h_at(i), vr = v_at(i);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    square = fmadd(hr[j] * f, hr[j] * f, square);
-                    dot = fmadd(vr[j] * wr[j], hr[j] * f, dot);
+                    for (int j = 0; j < 8; ++j) ymost = Max{}(ymost, magnitude(yr[j]));
                 }
+                in_turn();
             }
-            reduce3<TPR>(square, dot, none, sums[1]);
-            mean = square / float(n) + a.eps * f * f;
+            f = rescale(block_reduce<TPR>(most, Max{}, tops[parity][0]));
+            if constexpr (POST) yf = rescale(block_reduce<TPR>(ymost, Max{}, tops[parity][1]));
+            sum = reduce<TPR, POST>(sum_up(f, yf), again[parity]);
+            mean = sum.h2 / float(n) + a.eps * f * f;
+            if constexpr (POST) ymean = sum.y2 / float(n) + a.eps * yf * yf;
         }
-        const float rs = inverse_root(mean), s = f * rs, back = rs * (dot / float(n));
-        float yf = 1, rt = 1;
+        // with h f and rs = 1 / rms(h f): s = f rs, and h s = (h f) rs; likewise for y
+        const float rs = inverse_root(mean), s = f * rs, back = rs * (sum.eh / float(n));
+        [[maybe_unused]] float rt = 1, ts = 1, yback = 0;
         if constexpr (POST) {
-            float ymean = ysquare / float(n) + a.eps;
-            if (!mean_in_range(ymean)) {
-                uint32_t most = 0;
-#pragma unroll
-                for (int i = 0; i < VPT; ++i) {
-                    const Raw8<T> yr = y_at(i);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) most = Max{}(most, magnitude(yr[j]));
-                }
-                yf = rescale(block_reduce<TPR>(most, Max{}, tops[1]));
-                ysquare = 0;
-#pragma unroll
-                for (int i = 0; i < VPT; ++i) {
-                    const Raw8<T> yr = y_at(i);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) ysquare = fmadd(yr[j] * yf, yr[j] * yf, ysquare);
-                }
-                if constexpr (S::waves > 1) __syncthreads();    // sums[0] has been read
-                float none = 0, nothing = 0;
-                reduce3<TPR>(ysquare, none, nothing, sums[0]);
-                ymean = ysquare / float(n) + a.eps * yf * yf;
-            }
-            rt = inverse_root(ymean);
+            rt = inverse_root(ymean), ts = yf * rt;
+            yback = rt * ((sum.kd + s * (sum.ke - rs * (back * sum.kh))) / float(n));
         }
-        keep_packed();
-        const T* const gate = static_cast<const T*>(a.gate);
-        float d[VPT][8];                                        // a
-        [[maybe_unused]] float ydot = 0;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const Raw8<T> wr = at(w, 0, 0, i), hr = h_at(i), vr = v_at(i), yr = y_at(i);
-            Raw8<T> er;
-            if constexpr (AHEAD) er = ekept[i];
-            else if (a.dh) er = at(a.dh, row, a.lddh, i);
+            const Raw8<T> hr = h_at(i), vr = v_at(i), wr = w_at(i);
+            float d[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float unit = hr[j] * f * rs, g = vr[j];
-                wsum[i][j] = fmadd(g, unit, wsum[i][j]);
-                d[i][j] = s * (g * wr[j] - unit * back);
+                const float unit = hr[j] * f * rs, v = vr[j];
+                wsum[i][j] = fmadd(v, unit, wsum[i][j]);
+                d[j] = s * (v * wr[j] - unit * back);
             }
             if (a.dh) {
+                const Raw8<T> dr = d_at(i);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) d[i][j] += er[j];
+                for (int j = 0; j < 8; ++j) d[j] += dr[j];
             }
-            float unit[8];
+            float dx[8], z[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                unit[j] = POST ? yr[j] * yf * rt : yr[j];
-                gsum(i, j) = fmadd(d[i][j], unit[j], gsum(i, j));
-            }
-            if constexpr (POST) {
-                const Raw8<T> pr = at(post, 0, 0, i);
-                float dots = 0;
-                if (a.gate) {
-                    const Raw8<T> gr = at(gate, gate_row, a.ldg, i);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) dots = fmadd(d[i][j] * gr[j] * pr[j], unit[j], dots);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) dots = fmadd(d[i][j] * pr[j], unit[j], dots);
-                }
-                ydot += dots;
-            }
-            in_turn<AHEAD>();
-        }
-        if constexpr (POST) ydot = block_reduce<TPR>(ydot, Add{}, ysums) / float(n);
-        keep_packed();
-        asm volatile("" : "+v"(rt));                            // y t is computed again: not kept from above
-        const bool last = !runs.of_gate && a.gate && ++in_gate == a.per;    // of a gate, in a run of whole gates
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
+            for (int j = 0; j < 8; ++j) dx[j] = a.c * d[j];
+            const Raw8<T> yr = y_at(i);                         // before the stores: dx or dy may be y
+            if constexpr (!HOLD) put(a.dx, row, a.lddx, i, dx);
+            in_turn();
             Raw8<T> pr, gr;
-            if constexpr (POST) pr = at(post, 0, 0, i);
-            if (a.gate) gr = at(gate, gate_row, a.ldg, i);
-            float dx[8], dy[8];
+            if constexpr (POST) pr = p_at(i);
+            if (a.gate) gr = g_at(i);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                dx[j] = a.c * d[i][j];
-                dy[j] = a.gate ? d[i][j] * gr[j] : d[i][j];
+                z[j] = POST ? yr[j] * yf * rt : yr[j];
+                gsum(i, j) = fmadd(d[j], z[j], gsum(i, j));
+            }
+            if (a.gate) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) d[j] *= gr[j];
             }
             if constexpr (POST) {
-                const Raw8<T> yr = y_at(i);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) dy[j] = yf * rt * (dy[j] * pr[j] - yr[j] * yf * rt * ydot);
+                for (int j = 0; j < 8; ++j) d[j] = ts * (d[j] * pr[j] - z[j] * yback);
             }
-            put(a.dx, row, a.lddx, i, dx);
-            put(a.dy, row, a.lddy, i, dy);
+            if constexpr (HOLD) put(a.dx, row, a.lddx, i, dx);
+            put(a.dy, row, a.lddy, i, d);
             if (last) {
                 float out[8];
 #pragma unroll
@@ -425,25 +477,18 @@ __global__ __launch_bounds__(Shape<TPR>::threads) void block_grad_kernel(BlockGr
                 if (a.dgate && a.dgtype == Type::F32) store8(static_cast<float*>(a.dgate) + gate_row * a.lddg + c, out, n - c);
                 else if (a.dgate) put(a.dgate, gate_row, a.lddg, i, out);
             }
-            in_turn<AHEAD>();
+            in_turn();
         }
         if (last) {
             in_gate = 0;
             ++gate_row;
-        }
-        if constexpr (S::waves > 1) __syncthreads();            // the next row's sums
-    }
-    // a run's S, or the workgroup's sums of dw and dpost
-    if (runs.of_gate && second && run < runs.count) {
+            if (AHEAD && row + 1 < end) {
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int c = 8 * (i * TPR + t);
-            float out[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) out[j] = gsum(i, j);
-            store8(second + run * n + c, out, n - c);
+                for (int i = 0; i < VPT; ++i) gk[i] = at(a.gate, gate_row, a.ldg, i);
+            }
         }
     }
+    // the workgroup's sums of dw, and of S or dpost
     auto store_sum = [&](float* to, const float (&sum)[VPT][8]) {
         if constexpr (S::rows == 1) {
 #pragma unroll
@@ -468,62 +513,68 @@ __global__ __launch_bounds__(Shape<TPR>::threads) void block_grad_kernel(BlockGr
         }
     };
     if (dw) store_sum(dw + int64_t(blockIdx.x) * n, wsum);
-    if (!runs.of_gate && second) {
+    if (second) {
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) wsum[i][j] = a.gate ? psum[i][j][threadIdx.x] : gsum(i, j);
+            for (int j = 0; j < 8; ++j) wsum[i][j] = a.gate && !runs.of_gate ? psum[i][j][threadIdx.x] : gsum(i, j);
         store_sum(second + int64_t(blockIdx.x) * n, wsum);
     }
 }
 
 // What is added up from the workspace: blockIdx.y 0: dw, 1: dpost, 2 + g: dgate of
-// gate g.  32 columns and 8 slices of the sums per workgroup, joined in LDS; eight
-// loads of a slice are on their way at a time.
+// gate g, which has `of_gate` of the workgroups' sums (0: it is written already).  32
+// columns and 32 slices of the sums per workgroup, joined in LDS, eight loads of a slice
+// on their way at a time: it is bound by their latency.
 template <typename T>
-__global__ __launch_bounds__(256) void block_grad_sums_kernel(BlockGradArgs a, Runs runs, const float* first, const float* second,
-                                                              int64_t groups) {
-    __shared__ float slice[8][33];
+__global__ __launch_bounds__(1024) void block_grad_sums_kernel(BlockGradArgs a, const float* first, const float* second, int groups,
+                                                               int of_gate) {
+    constexpr int SLICES = 32;
+    __shared__ float slice[SLICES][33];
     const int n = int(a.n), x = threadIdx.x & 31, y = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + x;
     const int what = int(blockIdx.y);
-    const float* from = what ? second : first;
-    int64_t count = groups;
-    if (what && runs.of_gate) {
-        count = what == 1 ? runs.count : runs.of_gate;
-        if (what > 1) from += (what - 2) * runs.of_gate * n;
-    }
-    const bool weighted = what == 1 && runs.of_gate;            // dpost = sum over gates of gate S
-    const T* gate = static_cast<const T*>(a.gate);
     if (what == 0 ? !a.dw : what == 1 ? !a.dpost : !a.dgate) return;
+    const float* from = what ? second : first;
+    int count = groups;
+    if (what > 1) {
+        count = of_gate;
+        from += int64_t(what - 2) * of_gate * n;
+    }
+    const bool weighted = what == 1 && of_gate;                 // dpost = sum over gates of gate S
+    const T* const gate = static_cast<const T*>(a.gate);
     float sum = 0;
     if (c < n) {
-        auto one = [&](int64_t p) {
-            const float v = from[p * n + c];
-            return weighted ? v * float(gate[p / runs.of_gate * a.ldg + c]) : v;
+        auto add = [&](auto some) {                             // up to eight of them
+            constexpr int MOST = decltype(some)::value;
+            return [&, MOST](int p) {
+                float v[MOST];
+#pragma unroll
+                for (int i = 0; i < MOST; ++i) v[i] = from[int64_t(p + SLICES * i) * n + c];
+                if (weighted) {
+#pragma unroll
+                    for (int i = 0; i < MOST; ++i) v[i] *= float(gate[int64_t((p + SLICES * i) / of_gate) * a.ldg + c]);
+                }
+#pragma unroll
+                for (int i = 0; i < MOST; ++i) sum += v[i];
+            };
         };
-        int64_t p = y;
-        for (; p + 56 < count; p += 64) {
-            float v[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = one(p + 8 * i);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sum += v[i];
-        }
-        for (; p < count; p += 8) sum += one(p);
+        int p = y;
+        for (; p + 7 * SLICES < count; p += 8 * SLICES) add(ic<8>{})(p);
+        for (; p < count; p += SLICES) add(ic<1>{})(p);
     }
     slice[y][x] = sum;
     __syncthreads();
     if (y == 0 && c < n) {
 #pragma unroll
-        for (int i = 1; i < 8; ++i) sum += slice[i][x];
+        for (int i = 1; i < SLICES; ++i) sum += slice[i][x];
         if (what == 0) {
             a.dw[c] = sum;
         } else if (what == 1) {
             a.dpost[c] = sum;
         } else {
             if (a.post) sum *= float(static_cast<const T*>(a.post)[c]);
-            const int64_t to = (what - 2) * a.lddg + c;
+            const int64_t to = int64_t(what - 2) * a.lddg + c;
             if (a.dgtype == Type::F32) static_cast<float*>(a.dgate)[to] = sum;
             else static_cast<T*>(a.dgate)[to] = T(sum);
         }
@@ -561,18 +612,20 @@ inline hipError_t block_norm_t(Scale sc, const BlockNormArgs& a, hipStream_t s) 
     });
 }
 
-// Runs of rows: two workgroups a compute unit, not less than four rows to a run.
-// A gate with more rows is cut into equal runs, smaller ones are put together.
+// Runs of rows: two workgroups a compute unit, or the one that it has registers for.  A
+// gate with more rows than a workgroup's groups of threads is cut into equal runs, whole
+// workgroups of them, so that its S is joined there; smaller ones are put together.  Runs
+// of one row, where there are few rows, cost the sums less than they save here: 64 rows
+// of 4096 take 8 + 4 us, in runs of two 12 + 4.
 template <int TPR>
 inline Runs make_runs(int64_t rows, int64_t per) {
-    const int64_t slots = 512 * Shape<TPR>::rows;
-    int64_t want = (rows + slots - 1) / slots;
-    if (want < 4) want = 4;
+    constexpr int64_t groups = Shape<TPR>::rows, slots = (TPR <= 256 ? 512 : 256) * groups;
+    const int64_t want = (rows + slots - 1) / slots;
     Runs r{want, 0, 0};
-    if (per > want) {
-        const int64_t parts = (per + want - 1) / want;
+    if (per > want && per > groups) {
+        const int64_t parts = (per + want * groups - 1) / (want * groups) * groups;
         r.rows = (per + parts - 1) / parts;
-        r.of_gate = (per + r.rows - 1) / r.rows;
+        r.of_gate = ((per + r.rows - 1) / r.rows + groups - 1) / groups * groups;
         r.count = rows / per * r.of_gate;
     } else {
         if (per > 0) r.rows = (want + per - 1) / per * per;
@@ -581,8 +634,11 @@ inline Runs make_runs(int64_t rows, int64_t per) {
     return r;
 }
 
-// Shapes of the gradient: as many threads as leave room for the next row, as above
-// for short rows.
+// Shapes of the gradient: the fewest threads whose registers have room for the next row,
+// so that two rows or more are under way on a compute unit.  In bf16, 8192 rows of 4096
+// take 97 us in 256 threads and 106 in 512; 4096 rows of 8192 96 us in 512 and 151 in
+// 1024, which have no room; 2048 rows of 16384, for which there is none, 153 us in 1024
+// and 181 in 512.
 template <typename T, typename F>
 inline hipError_t with_block_grad_shape(int64_t n, F&& f) {
     const int64_t v = (n + 7) / 8;
@@ -597,7 +653,8 @@ inline hipError_t with_block_grad_shape(int64_t n, F&& f) {
         if (v <= 512) return f(ic<512>{}, ic<1>{});
     }
     if (v <= 1024) return f(ic<512>{}, ic<2>{});
-    return f(ic<512>{}, ic<4>{});
+    if constexpr (sizeof(T) == 2) return f(ic<1024>{}, ic<2>{});
+    else return f(ic<512>{}, ic<4>{});
 }
 
 template <typename T, typename F>
@@ -612,8 +669,8 @@ inline auto with_runs(int64_t rows, int64_t n, int64_t per, F&& f) {
 template <typename T>
 inline int64_t block_norm_grad_floats_t(int64_t rows, int64_t n, int64_t per) {
     int64_t floats = 0;
-    with_runs<T>(rows, n, per, [&](auto, auto, const Runs& r, int64_t groups) {
-        floats = (groups + (r.of_gate ? r.count : groups)) * n;
+    with_runs<T>(rows, n, per, [&](auto, auto, const Runs&, int64_t groups) {
+        floats = 2 * groups * n;
         return hipSuccess;
     });
     return floats;
@@ -631,10 +688,11 @@ inline hipError_t block_norm_grad_t(const BlockGradArgs& a, hipStream_t s) {
         const hipError_t e = a.post ? launch(block_grad_kernel<T, TPR, VPT, true>, grid, block, 0, s, a, r, first, second)
                                     : launch(block_grad_kernel<T, TPR, VPT, false>, grid, block, 0, s, a, r, first, second);
         if (e != hipSuccess || (!first && !second)) return e;
-        const int64_t gates = r.of_gate && a.dgate ? r.count / r.of_gate : 0;
+        const int of_gate = int(r.of_gate / Shape<TPR>::rows);
+        const int64_t gates = of_gate && a.dgate ? a.rows / a.per : 0;
         const dim3 sums(uint32_t((a.n + 31) / 32), uint32_t(gates ? 2 + gates : a.dpost ? 2 : 1));
-        return launch(block_grad_sums_kernel<T>, sums, dim3(256), 0, s, a, r, static_cast<const float*>(a.workspace),
-                      static_cast<const float*>(second), groups);
+        return launch(block_grad_sums_kernel<T>, sums, dim3(1024), 0, s, a, static_cast<const float*>(a.workspace),
+                      static_cast<const float*>(second), int(groups), of_gate);
     });
 }
 

@@ -7,6 +7,43 @@
 namespace bl {
 namespace layer {
 
+// Eight elements from column c on of a row of n, in two parts: fetch() is one load of all
+// lanes without a branch, so that many may be on their way; settle(), where they are used,
+// puts them right in the lanes at the row's end.  Those load the row's last eight, which
+// settle() moves to the front, with zeros after them (only zeros past the end); what they
+// load of a neighbour's elements is dropped, so that the neighbour may have stored over it.
+template <typename T>
+__device__ __forceinline__ Raw8<T> fetch(const T* row, int c, int n) {
+    if (n < 8) return load8(row + c, n - c);
+    Raw8<T> r;
+    __builtin_memcpy(&r, row + (c < n - 8 ? c : n - 8), sizeof(r));
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ void settle(Raw8<T>& r, int c, int n) {
+    const int by = c + 8 - n;                                   // elements to move by
+    if (by <= 0 || n < 8) return;
+    constexpr int WORDS = 2 * sizeof(T);
+    auto words = [&](int by_words) {                            // a constant
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) r.word[i] = i + by_words < WORDS ? r.word[i + by_words] : 0;
+    };
+    if (by & 4) words(int(sizeof(T)));
+    if (by & 2) words(int(sizeof(T)) / 2);
+    if (by & 1) {
+        if constexpr (sizeof(T) == 4) {
+            words(1);
+        } else {
+#pragma unroll
+            for (int i = 0; i < WORDS; ++i) r.word[i] = __builtin_amdgcn_alignbit(i + 1 < WORDS ? r.word[i + 1] : 0, r.word[i], 16);
+        }
+    }
+    if (by >= 8) {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) r.word[i] = 0;
+    }
+}
+
 constexpr float kCodeMax = 127.0f;
 
 // The scale of a row from the bits of its largest magnitude: NaN where that is not finite.

@@ -162,9 +162,11 @@ def block_norm(y, residual, weight, post_weight=None, gate=None, *, residual_sca
     w = _vector(weight, "weight", dt, n)
     p = _vector(post_weight, "post_weight", dt, n) if post_weight is not None else None
     gp, gates, ldg = _gate(gate, rows, n, dt)
+    ldh = n
     if residual_out is None:
-        residual_out = torch.empty_like(residual)
-    ldh = _rows(residual_out, "residual_out", dt, (rows, n))[2]
+        residual_out = residual.new_empty(residual.shape)
+    else:
+        ldh = _rows(residual_out, "residual_out", dt, (rows, n))[2]
     sp = None
     if int8:
         if out is None:
@@ -178,9 +180,11 @@ def block_norm(y, residual, weight, post_weight=None, gate=None, *, residual_sca
     else:
         if scales is not None:
             raise ValueError("scales are for int8=True")
+        ldv = n
         if out is None:
-            out = torch.empty_like(y)
-        ldv = _rows(out, "out", dt, (rows, n))[2]
+            out = y.new_empty(y.shape)
+        else:
+            ldv = _rows(out, "out", dt, (rows, n))[2]
     s = _place(at, (residual, weight, post_weight, gate, residual_out, out, scales))
     st = lib.batchlas_block_norm(ty, 1 if int8 else 0, rows, n, y.data_ptr(), ldy, residual.data_ptr(), ldx, w, p, gp,
                                  gates, ldg, residual_scale, eps, residual_out.data_ptr(), ldh, out.data_ptr(), ldv, sp, s)
@@ -216,12 +220,15 @@ def block_norm_grad(dv, y, h, weight, post_weight=None, gate=None, dh=None, *, r
     p = _vector(post_weight, "post_weight", dt, n) if post_weight is not None else None
     gp, gates, ldg = _gate(gate, rows, n, dt)
     lddh = _rows(dh, "dh", dt, (rows, n))[2] if dh is not None else 0
+    lddy = lddx = n
     if dy is None:
-        dy = torch.empty_like(y)
-    lddy = _rows(dy, "dy", dt, (rows, n))[2]
+        dy = y.new_empty(y.shape)
+    else:
+        lddy = _rows(dy, "dy", dt, (rows, n))[2]
     if dx is None:
-        dx = torch.empty_like(h)
-    lddx = _rows(dx, "dx", dt, (rows, n))[2]
+        dx = h.new_empty(h.shape)
+    else:
+        lddx = _rows(dx, "dx", dt, (rows, n))[2]
     dgp, dgt, lddg = None, 0, 0
     if gate is None:
         if dgate is not None and dgate is not False:
@@ -230,29 +237,33 @@ def block_norm_grad(dv, y, h, weight, post_weight=None, gate=None, dh=None, *, r
     elif dgate is False:
         dgate = None
     else:
+        lddg = n
         if dgate is None:
-            dgate = torch.empty_like(gate, dtype=_F32 if gate.dim() == 1 else dt)
-        dgt = _TYPES.get(dgate.dtype, -1)
-        if dgate.dtype is not _F32 and dgate.dtype is not dt:
-            raise TypeError(f"dgate must be float32 or {dt}, not {dgate.dtype}")
-        lddg = _rows(dgate, "dgate", None, (gates, n))[2]
+            dgate = gate.new_empty(gate.shape, dtype=_F32 if gate.dim() == 1 else dt)
+        else:
+            if dgate.dtype is not _F32 and dgate.dtype is not dt:
+                raise TypeError(f"dgate must be float32 or {dt}, not {dgate.dtype}")
+            lddg = _rows(dgate, "dgate", None, (gates, n))[2]
+        dgt = 0 if dgate.dtype is _F32 else ty
         dgp = dgate.data_ptr()
     wp = pp = None
-    if dweight is False:
+    if dweight is None:
+        dweight = y.new_empty(n, dtype=_F32)
+        wp = dweight.data_ptr()
+    elif dweight is False:
         dweight = None
     else:
-        if dweight is None:
-            dweight = y.new_empty(n, dtype=_F32)
         wp = _vector(dweight, "dweight", _F32, n)
     if post_weight is None:
         if dpost_weight is not None and dpost_weight is not False:
             raise ValueError("dpost_weight needs a post_weight")
         dpost_weight = None
+    elif dpost_weight is None:
+        dpost_weight = y.new_empty(n, dtype=_F32)
+        pp = dpost_weight.data_ptr()
     elif dpost_weight is False:
         dpost_weight = None
     else:
-        if dpost_weight is None:
-            dpost_weight = y.new_empty(n, dtype=_F32)
         pp = _vector(dpost_weight, "dpost_weight", _F32, n)
     kp, size = None, 0
     if workspace is not None:

@@ -536,7 +536,7 @@ def test_block_norm_grad_what_is_asked_for():
 
 
 @pytest.mark.parametrize("t", TYPES)
-@pytest.mark.parametrize("n", [100, 3000, 16000])
+@pytest.mark.parametrize("n", [100, 101, 3000, 3003, 5005, 16000, 16003])
 def test_block_norm_grad_in_place_and_strided(t, n):
     import torch
     import dense_linear_algebra_potrf_amd as bl
@@ -586,6 +586,18 @@ def test_block_norm_grad_masks_and_ranges(t, n):
             assert torch.equal(a[[0, 1, 2, 3, 4, 7]], b[[0, 1, 2, 3, 4, 7]])
         assert torch.equal(bad[2][0], got[2][0])
         assert bool(torch.isnan(bad[1][5]).all())
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [60, 700, 5000, 16000])
+@pytest.mark.parametrize("of_rows,of_gradients", [(1e12, 1e27), (1e-12, 1e-27)])
+def test_block_norm_grad_products_leave_the_range(t, n, of_rows, of_gradients):
+    """Neither the rows' squares, the gradients nor the results leave 32 bits, but the rows' products with the gradients."""
+    import dense_linear_algebra_potrf_amd as bl
+    announce("block_norm_grad products", t, n, of_rows)
+    dv, y, h, w, p, g, dh = grad_inputs(11, dtype(t), 6, n, True, 2, True)
+    inputs = dv * of_gradients, y * of_rows, h * of_rows, w, p, g, dh * of_gradients
+    check_grad(inputs, 1.0, 0.0, bl.block_norm_grad(*inputs, eps=0.0))
 
 
 # ---------------------------------------------------------------- together
