@@ -245,7 +245,8 @@ _LAZY = {"rmsnorm_quant": "layer", "rmsnorm_grad": "layer", "rmsnorm_grad_worksp
          "weight_quant": "layer", "weight_matvec": "layer", "weight_matvec_workspace": "layer",
          "int8_quant": "integer", "int8_matmul": "integer", "block_norm": "integer",
          "block_norm_grad": "integer", "block_norm_grad_workspace": "integer",
-         "calibrate_weights": "calibrate", "second_moments": "calibrate"}
+         "calibrate_weights": "calibrate", "calibrate_channels": "calibrate",
+         "second_moments": "calibrate"}
 
 
 def __getattr__(name: str):
