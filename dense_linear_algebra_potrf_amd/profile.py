@@ -19,7 +19,8 @@ HBM traffic per launch that bench.py attaches to its roofline while the
 family's sources are unchanged.
 
 `python -m dense_linear_algebra_potrf_amd.profile --raw DIR --out DIR --layer` does the same for the listed
-cases of perf/operators.py (the low-bit layer operators), into layer_operators.md.
+cases of perf/operators.py (the low-bit layer operators), into layer_operators.md, and `--integer` for those
+of perf/more_operators.py (the 8-bit-integer layer operators), into integer_operators.md.
 """
 from __future__ import annotations
 
@@ -278,10 +279,17 @@ def summary_md(name, cfg, stats, kern, vals, rec, cmds) -> str:
     return "\n".join(lines)
 
 
-# ---------------------------------------------------------------- the low-bit layer operators
-LAYER_KERNELS = "rmsnorm_|weight_|pack_kernel"
-LAYER_NAMES = ("rmsnorm_quant_kernel", "rmsnorm_grad_kernel", "rmsnorm_dw_kernel", "weight_quant_kernel", "weight_matvec_kernel",
-               "weight_many_kernel", "pack_kernel")
+# ---------------------------------------------------------------- the layer operators
+# what --layer and --integer profile: the file of cases, its title, the kernels (a regex and
+# their names), and the summary
+LAYERS = {
+    "layer": ("operators", "the low-bit layer operators", "rmsnorm_|weight_|pack_kernel",
+              ("rmsnorm_quant_kernel", "rmsnorm_grad_kernel", "rmsnorm_dw_kernel", "weight_quant_kernel", "weight_matvec_kernel",
+               "weight_many_kernel", "pack_kernel"), "layer_operators.md"),
+    "integer": ("more_operators", "the 8-bit-integer layer operators", "int8_|block_norm_|block_grad_",
+                ("int8_quant_kernel", "int8_quant_long_kernel", "int8_quant_given_kernel", "int8_few_kernel", "int8_tiles_kernel",
+                 "block_norm_kernel", "block_grad_kernel", "block_grad_sums_kernel"), "integer_operators.md"),
+}
 LAYER_PASSES = [
     ["FETCH_SIZE"],
     ["WRITE_SIZE", "GRBM_GUI_ACTIVE"],
@@ -290,24 +298,25 @@ LAYER_PASSES = [
 ]
 
 
-def layer_module():
+def layer_module(which: str):
     import importlib.util
-    spec = importlib.util.spec_from_file_location("operators", os.path.join(ROOT, "perf", "operators.py"))
+    name = LAYERS[which][0]
+    spec = importlib.util.spec_from_file_location(name, os.path.join(ROOT, "perf", name + ".py"))
     m = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(m)
     m.own = True
     return m
 
 
-def layer_name(name: str) -> str:
+def layer_name(which: str, name: str) -> str:
     """The kernel's own name: the profiler does not spell the 16-bit element types in its template arguments."""
-    return next(k for k in LAYER_NAMES if k in name)
+    return next((k for k in LAYERS[which][3] if k in name), None)
 
 
-def run_layer_case(name: str, passes: int) -> None:
+def run_layer_case(which: str, name: str, passes: int) -> None:
     """The program under the profiler: passes through a listed case, on three sets of inputs in turn."""
     import torch
-    m = layer_module()
+    m = layer_module(which)
     case = next(c for c in m.listed() if c["name"] == name)
     states = [m.prepare(case, seed) for seed in (1, 2, 3)]
     for i in range(passes):
@@ -316,19 +325,21 @@ def run_layer_case(name: str, passes: int) -> None:
     print(f"ran {name}", flush=True)
 
 
-def profile_layer(raw: str, outdir: str, ffac: float, wfac: float, calib_cmds: list[str]) -> None:
-    m = layer_module()
-    cmd = lambda name, passes: ["python3", os.path.abspath(__file__), "--run-layer", name, "--passes", str(passes)]  # noqa: E731
+def profile_layer(which: str, raw: str, outdir: str, ffac: float, wfac: float, calib_cmds: list[str]) -> None:
+    m = layer_module(which)
+    cases, title, regex, _, summary = LAYERS[which]
+    cmd = lambda name, passes: ["python3", os.path.abspath(__file__), f"--{which}", "--run-layer", name,  # noqa: E731
+                                "--passes", str(passes)]
     rows, kernels = [], []
     for case in m.listed():
         name, work = case["name"], m.work(case)
         out = run_rocprof(["--kernel-trace", "--stats"], cmd(name, 60), os.path.join(raw, f"{name}_stats"))
-        mine = [s for s in kernel_stats(out) if any(k in s["name"] for k in LAYER_KERNELS.split("|"))]
+        mine = [s for s in kernel_stats(out) if layer_name(which, s["name"])]
         if not mine:
             raise RuntimeError(f"no library kernel in the trace of {name}")
         sums: dict[str, float] = {}
         for i, group in enumerate(LAYER_PASSES):
-            out = run_rocprof(["--pmc", *group, "--kernel-include-regex", LAYER_KERNELS], cmd(name, 6),
+            out = run_rocprof(["--pmc", *group, "--kernel-include-regex", regex], cmd(name, 6),
                               os.path.join(raw, f"{name}_pmc{i}"))
             for s in mine:
                 for k, v in counters(out, s["name"]).items():
@@ -342,28 +353,30 @@ def profile_layer(raw: str, outdir: str, ffac: float, wfac: float, calib_cmds: l
                     f"{100 * sums['SQ_LDS_IDX_ACTIVE'] / (gui * CUS):.0f}% | "
                     f"{100 * sums['SQ_WAIT_INST_ANY'] / sums['SQ_WAVE_CYCLES']:.0f}% |")
         for s in mine:
-            kernels.append(f"| {name} | `{layer_name(s['name'])}` | {s['calls']} | {s['avg_us']:.2f} | {s['min_us']:.2f} | "
+            kernels.append(f"| {name} | `{layer_name(which, s['name'])}` | {s['calls']} | {s['avg_us']:.2f} | {s['min_us']:.2f} | "
                            f"{s['max_us']:.2f} |")
         print(f"[profile] {name}: {us:.2f} us", flush=True)
-    lines = ["# rocprofv3: the low-bit layer operators, listed cases of perf/operators.py", "",
-             "Written by `python -m dense_linear_algebra_potrf_amd.profile --raw <raw> --out profiles --layer`, which ran for",
+    lines = [f"# rocprofv3: {title}, listed cases of perf/{cases}.py", "",
+             f"Written by `python -m dense_linear_algebra_potrf_amd.profile --raw <raw> --out profiles --{which}`, which ran for",
              "each case, from /tmp with TMPDIR=/tmp on one MI355X (three sets of inputs in turn):", "", "```",
-             "rocprofv3 --kernel-trace --stats --output-format csv -d <out> -o run -- python3 profile.py --run-layer CASE --passes 60",
-             *[f"rocprofv3 --pmc {' '.join(g)} --kernel-include-regex '{LAYER_KERNELS}' --output-format csv -d <out> -o run -- "
-               "python3 profile.py --run-layer CASE --passes 6" for g in LAYER_PASSES], *calib_cmds, "```", "",
+             "rocprofv3 --kernel-trace --stats --output-format csv -d <out> -o run -- "
+             f"python3 profile.py --{which} --run-layer CASE --passes 60",
+             *[f"rocprofv3 --pmc {' '.join(g)} --kernel-include-regex '{regex}' --output-format csv -d <out> -o run -- "
+               f"python3 profile.py --{which} --run-layer CASE --passes 6" for g in LAYER_PASSES], *calib_cmds, "```", "",
              "A pass's kernels together; TB/s is the case's own bytes (each input read once, each output written once) over",
              "their time; busy fractions are of the SIMD (VALU, MFMA) and CU (LDS) cycles while the kernels ran, waiting is",
              "`SQ_WAIT_INST_ANY` over the wave cycles:", "",
              "| Case | Kernels (µs) | Bytes (MB) | TB/s | HBM read / written (MB) | VALU busy | MFMA busy | LDS busy | Waiting |",
              "|---|---|---|---|---|---|---|---|---|", *rows, "", "| Case | Kernel | Calls | Average (µs) | Min (µs) | Max (µs) |",
              "|---|---|---|---|---|---|", *kernels, ""]
-    with open(os.path.join(outdir, "layer_operators.md"), "w") as f:
+    with open(os.path.join(outdir, summary), "w") as f:
         f.write("\n".join(lines))
 
 
 def main(argv=None) -> int:
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--layer", action="store_true", help="profile the cases of perf/operators.py instead")
+    ap.add_argument("--integer", action="store_true", help="profile the cases of perf/more_operators.py instead")
     ap.add_argument("--run-layer", help=argparse.SUPPRESS)
     ap.add_argument("--passes", type=int, default=60, help=argparse.SUPPRESS)
     ap.add_argument("--raw", help="directory for rocprofv3's raw output")
@@ -372,8 +385,9 @@ def main(argv=None) -> int:
     ap.add_argument("--reparse", action="store_true",
                     help="rebuild the summaries from the raw output of an earlier run")
     a = ap.parse_args(argv)
+    which = "integer" if a.integer else "layer" if a.layer or a.run_layer else None
     if a.run_layer:
-        run_layer_case(a.run_layer, a.passes)
+        run_layer_case(which, a.run_layer, a.passes)
         return 0
     if not a.raw or not a.out:
         ap.error("--raw and --out are required")
@@ -384,8 +398,8 @@ def main(argv=None) -> int:
     os.makedirs(a.out, exist_ok=True)
     ffac, wfac, calib_cmds = calibrate(a.raw)
     print(f"[profile] calibration: FETCH_SIZE x{ffac:.3f}, WRITE_SIZE x{wfac:.3f}", flush=True)
-    if a.layer:
-        profile_layer(a.raw, a.out, ffac, wfac, calib_cmds)
+    if which:
+        profile_layer(which, a.raw, a.out, ffac, wfac, calib_cmds)
         return 0
     for name in a.config or [bench.PRIMARY] + bench.SECONDARY:
         profile_config(name, a.raw, a.out, ffac, wfac, calib_cmds)
