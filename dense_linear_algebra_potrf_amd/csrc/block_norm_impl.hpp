@@ -8,7 +8,7 @@
 // 8 (i TPR + t)) from its loads through both sums of squares to the stores.
 //
 // HBM bounds it: x, y, h and v (and a gate for each row), a pass each.  8192 rows of 8192
-// in bf16 take 121 us (a copy of as many bytes 104), with codes 110 (91), of 4096 57 (52).
+// in bf16 take 117 us (a copy of as many bytes 104), with codes 101 (91), of 4096 57 (52).
 #pragma once
 
 #include "integer_impl.hpp"
@@ -56,6 +56,13 @@ __device__ __forceinline__ float unit_factor(float (&v)[VPT][8], int n, float ep
     return inverse_root(mean);
 }
 
+// The weights and the gate are on their way before the sums that they wait for, where
+// that costs few of the wavefronts a compute unit has room for: 8192 rows of 8192 in bf16 take
+// 117 us where they took 121, to codes 101 (110), of 4096 in f32 110 (119).  In shapes
+// where it costs more of them it loses: 65536 rows of 1024 114 (108), 2000 of 12000 with
+// a gate each 61 (58).
+template <int TPR, int VPT> constexpr bool kEarly = VPT == 1 || VPT == 4 || (VPT == 2 && TPR > 64);
+
 template <typename T, int TPR, int VPT, bool POST, bool CODES>
 __global__ __launch_bounds__(Shape<TPR>::threads) void block_norm_kernel(BlockNormArgs a) {
     using S = Shape<TPR>;
@@ -63,10 +70,12 @@ __global__ __launch_bounds__(Shape<TPR>::threads) void block_norm_kernel(BlockNo
     __shared__ uint32_t tops[3][S::waves];
     const int t = threadIdx.x % TPR;
     const int n = int(a.n);
+    constexpr bool EARLY = kEarly<TPR, VPT>;
     const T* w = static_cast<const T*>(a.w);
     // Where a row is shared by less than a wave, its end is in every wave's way: loads without
     // a branch take 124 us in place of 154 for 500000 rows of 100 in f16.  In longer rows
-    // the last threads alone take the branch, and 8192 rows of 8192 take 121 us with it, 127 without.
+    // the last threads alone take the branch, and 8192 rows of 8192 in bf16 took 121 us with it, 127
+    // without.
     auto at = [&](const T* from, int c) {
         if constexpr (TPR >= 64) return load8(from + c, n - c);
         Raw8<T> r = fetch(from, c, n);
@@ -89,17 +98,25 @@ __global__ __launch_bounds__(Shape<TPR>::threads) void block_norm_kernel(BlockNo
             for (int j = 0; j < 8; ++j) v[i][j] = yr[j];
         }
         [[maybe_unused]] float ts = 1;
+        Raw8<T> pk[VPT], gk[VPT], wk[VPT];
+        if constexpr (EARLY) {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                if constexpr (POST) pk[i] = at(static_cast<const T*>(a.post), 8 * (i * TPR + t));
+                if (a.gate) gk[i] = at(gate, 8 * (i * TPR + t));
+            }
+        }
         if constexpr (POST) ts = unit_factor<TPR>(v, n, a.eps, sums[0], sums[1], tops[0]);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int c = 8 * (i * TPR + t), left = n - c;
             if constexpr (POST) {
-                const Raw8<T> p = at(static_cast<const T*>(a.post), c);
+                const Raw8<T> p = EARLY ? pk[i] : at(static_cast<const T*>(a.post), c);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * ts * p[j];
             }
             if (a.gate) {
-                const Raw8<T> g = at(gate, c);
+                const Raw8<T> g = EARLY ? gk[i] : at(gate, c);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[i][j] = fmadd(v[i][j], g[j], a.c * held[i][j]);
             } else {
@@ -111,12 +128,16 @@ __global__ __launch_bounds__(Shape<TPR>::threads) void block_norm_kernel(BlockNo
             for (int j = 0; j < 8; ++j) v[i][j] = j < left ? v[i][j] : 0.0f;
             store8(static_cast<T*>(a.h) + row * a.ldh + c, v[i], left);
         }
+        if constexpr (EARLY) {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) wk[i] = at(w, 8 * (i * TPR + t));
+        }
         const float rs = unit_factor<TPR>(v, n, a.eps, sums[2], sums[3], tops[1]);
         uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int c = 8 * (i * TPR + t), left = n - c;
-            const Raw8<T> wr = at(w, c);
+            const Raw8<T> wr = EARLY ? wk[i] : at(w, c);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 v[i][j] = v[i][j] * rs * wr[j];
