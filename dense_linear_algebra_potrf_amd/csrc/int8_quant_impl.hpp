@@ -36,7 +36,7 @@ __device__ __forceinline__ void round_store(const Int8QuantArgs& a, int64_t row,
     if (a.values) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) q[j] *= scale;
-        store8(static_cast<T*>(a.values) + row * a.ldv + c, q, left);
+        store8_past(static_cast<T*>(a.values) + row * a.ldv + c, q, left);
     }
 }
 
