@@ -11,8 +11,8 @@
 // whole 128-byte line of memory.
 //
 // W is the product's first operand, so that a lane's four sums are neighbouring
-// columns of y, and the rows of W are dealt to a wavefront's NI tiles by fours, so
-// that its 4 NI sums of a row of x are.
+// columns of y.  In 16 bits, and in the kernel for few rows, the rows of W are dealt to a
+// wavefront's NI tiles by fours, so that its 4 NI sums of a row of x are.
 //
 // Columns past k are masked in x alone: zero times whatever W's padding holds is
 // zero in integers.  Rows past the end are those of the last one, not stored.
@@ -20,15 +20,15 @@
 // Few rows are bound by W's bytes, and run at or above a large copy's rate (5.1 TB/s;
 // several of these sizes stay in the last-level cache): 16 x 28672 x 8192 42.1 us a call,
 // 5.6 TB/s; 64 x 8192 x 8192 12.9, 5.3.  1 x 4096 x 4096 takes 4.5 in the kernel, 6.7 a call.
-// Many rows are bound by what a compute unit gets from the caches: 8192 x 8192 x 8192 459 us,
-// 2397 TOP/s, where without its loads the kernel takes 360 and without its products 430, and the
+// Many rows are bound by what a compute unit gets from the caches: 8192 x 8192 x 8192 451 us,
+// 2438 TOP/s, where without its loads the kernel took 360 and without its products 430, and the
 // matrix cores alone 233; the library's product of these integers (without scales) takes 496.
 // Measured there and not kept: half-width steps, four of them in LDS (500 us: half lines
 // load at half the rate); the two wavefronts of a SIMD in turns of reading and
 // multiplying (485); loads as whole-address loads, which the compiler lets every LDS
 // read wait for (510); loads after all products or before them (492, 462).
-// 517 x 5003 x 2500 takes 18.5, with rows of 2512 bytes, so that every piece of 128 columns
-// lies in two cache lines; with rows of 2560 it takes 17.0.
+// 517 x 5003 x 2500 in 32 bits takes 17.6, with rows of 2512 bytes, so that every piece of 128
+// columns lies in two cache lines; with rows of 2560 it takes 16.3.
 #pragma once
 
 #include "integer_impl.hpp"
@@ -97,14 +97,11 @@ __device__ __forceinline__ i32x4 first_bytes(int left) {
     return v;
 }
 
-// Columns c .. c + COUNT - 1 of a row of y from their sums: `left` of them, times the row's
-// scale and theirs.  Where the scales' product is not a normal number it says nothing of
-// theirs with the sum, which is then taken in 64 bits.  Tiles in 16 bits are stored past
-// the caches, which then keep more of x and W: 8192 x 28672 x 1024 takes 301 us in place of
-// 363, 1024 x 8192 x 8192 73 (80).  In 32 bits a lane's columns take four stores, each of
-// every fourth 16 bytes, and lose by it: 8192 x 8192 x 8192 700 (534).
+// COUNT columns of a row of y from their sums, times the row's scale and theirs.  Where the
+// scales' product is not a normal number it says nothing of theirs with the sum, which
+// is then taken in 64 bits.
 template <typename T, int COUNT>
-__device__ __forceinline__ void store_scaled(T* y, const int (&sum)[COUNT], float xs, const float (&ws)[COUNT], int left) {
+__device__ __forceinline__ void scaled(T (&t)[COUNT], const int (&sum)[COUNT], float xs, const float (&ws)[COUNT]) {
     float v[COUNT];
     bool odd = false;
 #pragma unroll
@@ -117,11 +114,15 @@ __device__ __forceinline__ void store_scaled(T* y, const int (&sum)[COUNT], floa
 #pragma unroll
         for (int i = 0; i < COUNT; ++i) v[i] = float(double(sum[i]) * double(xs) * double(ws[i]));
     }
-    T t[COUNT];
 #pragma unroll
     for (int i = 0; i < COUNT; ++i) t[i] = T(v[i]);
+}
+
+// The first `left` of COUNT neighbouring columns, past the caches where PAST.
+template <bool PAST, typename T, int COUNT>
+__device__ __forceinline__ void store_columns(T* y, const T (&t)[COUNT], int left) {
     if (left >= COUNT) {
-        if constexpr (sizeof(T) == 2 && COUNT >= 8) store_past(y, t);
+        if constexpr (PAST) store_past(y, t);
         else __builtin_memcpy(y, t, sizeof(t));
     } else {
 #pragma unroll
@@ -142,6 +143,7 @@ template <typename T, int MI, int NI, int WM, int WN, int DEPTH>
 __global__ __launch_bounds__(64 * WM * WN) void int8_tiles_kernel(Int8MatmulArgs a) {
     constexpr int WAVES = WM * WN, XT = MI * WM, WT = NI * WN;  // tiles of x and W
     constexpr int XLOADS = 2 * XT / WAVES, LOADS = XLOADS + 2 * WT / WAVES;     // a wavefront's, half a tile each
+    constexpr int DEAL = sizeof(T) == 2 ? NI : 1;               // tiles that rows of W are dealt to
     static_assert(2 * XT % WAVES == 0 && 2 * WT % WAVES == 0 && DEPTH >= 2);
     __shared__ __attribute__((aligned(16))) int8_t lds[DEPTH][(XT + WT) * kTile];
 
@@ -158,7 +160,7 @@ __global__ __launch_bounds__(64 * WM * WN) void int8_tiles_kernel(Int8MatmulArgs
 
     // which KB of a step's tiles each load fills (x's first), and where this lane's piece comes from
     auto place = [&](int i) { return i < XLOADS ? wave * XLOADS + i : 2 * XT + wave * (LOADS - XLOADS) + i - XLOADS; };
-    auto column = [&](int i) { return column_of(place(i) & 1, lane); };
+    auto piece = [&](int i) { return column_of(place(i) & 1, lane); };
     const int k16 = int((a.k + 15) / 16 * 16), steps = int((a.k + kStep - 1) / kStep), tail = int(a.k % kStep);
     uint32_t offset[LOADS];
 #pragma unroll
@@ -166,17 +168,17 @@ __global__ __launch_bounds__(64 * WM * WN) void int8_tiles_kernel(Int8MatmulArgs
         const int row = row_of(place(i) & 1, lane), tile = place(i) >> 1;
         if (i < XLOADS) {
             const int64_t at = 16 * tile + row, most = a.m - 1 - m0;
-            offset[i] = uint32_t((at < most ? at : most) * a.ldx) + column(i);
+            offset[i] = uint32_t((at < most ? at : most) * a.ldx) + piece(i);
         } else {
             const int t = tile - XT;
-            const int64_t at = t / NI * 16 * NI + 4 * NI * (row >> 2) + 4 * (t % NI) + (row & 3), most = a.n - 1 - n0;
-            offset[i] = uint32_t((at < most ? at : most) * a.ldw) + column(i);
+            const int64_t at = t / DEAL * 16 * DEAL + 4 * DEAL * (row >> 2) + 4 * (t % DEAL) + (row & 3), most = a.n - 1 - n0;
+            offset[i] = uint32_t((at < most ? at : most) * a.ldw) + piece(i);
         }
     }
     // Pieces past the row's end are the first one again.  Steps past the last one load nothing
     // (from no rows), so that the loads on their way can be counted.
     auto load = [&](int step, int8_t* to, int i) {
-        const int c = column(i), from = step * kStep;
+        const int c = piece(i), from = step * kStep;
         const bool whole = from + kStep <= k16;
         load_to_lds(rows_at(i < XLOADS ? x : w, step < steps), whole || c < k16 - from ? offset[i] : offset[i] - c, from, to + place(i) * 1024);
     };
@@ -197,7 +199,7 @@ __global__ __launch_bounds__(64 * WM * WN) void int8_tiles_kernel(Int8MatmulArgs
 #pragma unroll
             for (int i = 0; i < XLOADS; ++i) {
                 i32x4* p = reinterpret_cast<i32x4*>(lds[at] + place(i) * 1024 + 16 * lane);
-                if (column(i) + 16 > tail) *p &= first_bytes(tail - column(i));
+                if (piece(i) + 16 > tail) *p &= first_bytes(tail - piece(i));
             }
             wait_loads<LOADS * (DEPTH - 2)>();
         }
@@ -235,21 +237,40 @@ __global__ __launch_bounds__(64 * WM * WN) void int8_tiles_kernel(Int8MatmulArgs
     }
     wait_loads<0>();
 
-    const int64_t n = n0 + wn * 16 * NI + 4 * NI * g;
-    const int left = a.n - n < 4 * NI ? int(a.n - n) : 4 * NI;
+    // In 16 bits a lane's columns are neighbours; in 32 those of a row's four lanes are, 64 bytes a
+    // store: 717 x 14784 x 82 takes 15.1 us, with a lane's 64 bytes in four stores 26.8.
+    // All stores go past the caches, which keep more of x and W that way: 8192 x 28672 x 1024 in bf16
+    // takes 302 us in place of 363, 1024 x 8192 x 8192 73 (80).  A row's follow one another, so that
+    // they fill whole lines before these are sent on.
+    constexpr int COUNT = 4 * DEAL;                             // neighbouring columns
+    const int64_t n = n0 + wn * 16 * NI + COUNT * g;
+    const int left = a.n - n < 16 * NI ? int(a.n - n) : 16 * NI;
     if (left <= 0) return;
+    auto column = [](int c) { return c / COUNT * 4 * COUNT + c % COUNT; };
     float ws[4 * NI];
 #pragma unroll
-    for (int j = 0; j < 4 * NI; ++j) ws[j] = a.ws[j < left ? n + j : n];
+    for (int c = 0; c < 4 * NI; ++c) ws[c] = a.ws[column(c) < left ? n + column(c) : n];
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
         const int64_t m = m0 + (wm * MI + i) * 16 + r;
         if (m >= a.m) continue;
         int sum[4 * NI];
 #pragma unroll
-        for (int j = 0; j < 4 * NI; ++j) sum[j] = acc[i][j / 4][j % 4];
+        for (int c = 0; c < 4 * NI; ++c) sum[c] = acc[i][c / 4][c % 4];
         __builtin_amdgcn_sched_barrier(0);                      // row by row, for the registers
-        store_scaled(static_cast<T*>(a.y) + m * a.ldy + n, sum, a.xs[m], ws, left);
+        T t[NI / DEAL][COUNT];
+        scaled(reinterpret_cast<T (&)[4 * NI]>(t), sum, a.xs[m], ws);
+        T* const y = static_cast<T*>(a.y) + m * a.ldy + n;
+        if constexpr (DEAL == NI) {
+            store_columns<true>(y, t[0], left);
+        } else if (left > column(4 * NI - 1)) {
+#pragma unroll
+            for (int j = 0; j < NI / DEAL; ++j) store_past(y + 4 * COUNT * j, t[j]);
+        } else {
+#pragma unroll
+            for (int c = 0; c < 4 * NI; ++c)
+                if (column(c) < left) y[column(c)] = t[c / COUNT][c % COUNT];
+        }
     }
 }
 
@@ -366,7 +387,9 @@ __global__ __launch_bounds__(64 * WAVES) void int8_few_kernel(Int8MatmulArgs a) 
         float ws[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) ws[j] = a.ws[j < left ? n + j : n];
-        store_scaled(static_cast<T*>(a.y) + m * a.ldy + n, sum, a.xs[m], ws, left);
+        T t[4];
+        scaled(t, sum, a.xs[m], ws);
+        store_columns<false>(static_cast<T*>(a.y) + m * a.ldy + n, t, left);
     }
 }
 
