@@ -256,6 +256,8 @@ def weight_quant(W, *, format: str = "int4", group: int | None = None, zeros: bo
     groups = -(-k // group)
     if codes is None:
         codes = W.new_empty((n, (k + 31) // 32 * 16), dtype=torch.uint8)
+        if k % 32:                                              # the same bytes on every run, the padding too
+            codes[:, (k + 1) // 2:].zero_()
     if codes.shape[0] != n:
         raise ValueError(f"codes must have {n} rows")
     ldc = _codes(codes, k)[1]
