@@ -8,7 +8,8 @@
 // 8 (i TPR + t)) from its loads through both sums of squares to the stores.
 //
 // HBM bounds it: x, y, h and v (and a gate for each row), a pass each.  8192 rows of 8192
-// in bf16 take 117 us (a copy of as many bytes 104), with codes 101 (91), of 4096 57 (52).
+// in bf16 take 97 us (a copy of as many bytes 104), with codes 95 (91), of 4096 47 (52), in f32
+// 110 (104).
 #pragma once
 
 #include "integer_impl.hpp"
@@ -68,7 +69,8 @@ __device__ __forceinline__ void store_row(T* p, const float (&f)[8], int count) 
 
 // The weights and the gate are on their way before the sums that they wait for, where
 // that costs few of the wavefronts a compute unit has room for: 8192 rows of 8192 in bf16 take
-// 117 us where they took 121, to codes 101 (110), of 4096 in f32 110 (119).  In shapes
+// 117 us where they took 121, to codes 101 (110), of 4096 in f32 110 (119), all stored through
+// the caches.  In shapes
 // where it costs more of them it loses: 65536 rows of 1024 114 (108), 2000 of 12000 with
 // a gate each 61 (58).
 template <int TPR, int VPT> constexpr bool kEarly = VPT == 1 || VPT == 4 || (VPT == 2 && TPR > 64);
@@ -83,7 +85,7 @@ __global__ __launch_bounds__(Shape<TPR>::threads) void block_norm_kernel(BlockNo
     constexpr bool EARLY = kEarly<TPR, VPT>;
     const T* w = static_cast<const T*>(a.w);
     // Where a row is shared by less than a wave, its end is in every wave's way: loads without
-    // a branch take 124 us in place of 154 for 500000 rows of 100 in f16.  In longer rows
+    // a branch took 124 us in place of 154 for 500000 rows of 100 in f16 (98 now).  In longer rows
     // the last threads alone take the branch, and 8192 rows of 8192 in bf16 took 121 us with it, 127
     // without.
     auto at = [&](const T* from, int c) {
@@ -183,7 +185,7 @@ __global__ __launch_bounds__(Shape<TPR>::threads) void block_norm_kernel(BlockNo
 // With k = gate post y, the last mean comes apart into sums that need neither root nor
 // the other mean, so that a row takes one reduction and one barrier:
 //     sum(b post z) = t (sum(k dh) + s sum(k e) - s^2 mean(e u) sum(k h)).
-// (Three reductions, one after the other, took 130 us where this takes 97.)
+// (Three reductions, one after the other, took 130 us where this took 97.)
 //
 // Each group of TPR threads takes a run of consecutive rows and keeps its sums over
 // them in registers: runs either lie within one gate's rows, whose sums S then go to
@@ -192,8 +194,8 @@ __global__ __launch_bounds__(Shape<TPR>::threads) void block_norm_kernel(BlockNo
 // block_grad_sums_kernel: no atomics, so two runs agree bit for bit.
 //
 // HBM bounds it: dv, y, h and dh are read and dx and dy written once.  8192 rows of 4096 in bf16
-// with eight gates take 97 us, 89 of them here and 7 in the sums (a copy of as many
-// bytes 78), in f32 169 (157), 4096 of 8192 in bf16 96 (78).  517 rows of 1537 take
+// with eight gates take 95 us, 87 of them here and 8 in the sums (a copy of as many
+// bytes 78), in f32 168 (157), 4096 of 8192 in bf16 89 (78).  517 rows of 1537 take
 // 18 us, 11 here and 4 in the sums: the latency of two launches.
 struct Runs {
     int64_t rows;        // of a run
@@ -234,7 +236,7 @@ __device__ __forceinline__ RowSums reduce(RowSums v, RowSums* slot) {
 
 // What a shape's registers have room for: the weights over all rows and the next row
 // while this one is reduced and stored; or only this row; or not even that (it then comes
-// from the cache a second time, which rows beyond 8192 pay with 153 us where a copy takes 78).
+// from the cache a second time, which rows beyond 8192 pay with 135 us where a copy takes 78).
 template <typename T, int TPR, int VPT> constexpr bool kAhead = TPR <= 512 && VPT * sizeof(T) <= 4;
 template <typename T, int TPR, int VPT> constexpr bool kHold = TPR <= 512 && VPT <= 2;
 
@@ -670,9 +672,9 @@ inline Runs make_runs(int64_t rows, int64_t n, int64_t per) {
 
 // Shapes of the gradient: the fewest threads whose registers have room for the next row,
 // so that two rows or more are under way on a compute unit.  In bf16, 8192 rows of 4096
-// take 97 us in 256 threads and 106 in 512; 4096 rows of 8192 96 us in 512 and 151 in
+// took 97 us in 256 threads and 106 in 512; 4096 rows of 8192 96 us in 512 and 151 in
 // 1024, which have no room; 2048 rows of 16384, for which there is none, 153 us in 1024
-// and 181 in 512.
+// and 181 in 512 (before the stores past the caches).
 template <typename T, typename F>
 inline hipError_t with_block_grad_shape(int64_t n, F&& f) {
     const int64_t v = (n + 7) / 8;

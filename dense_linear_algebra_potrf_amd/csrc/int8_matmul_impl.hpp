@@ -20,8 +20,8 @@
 // Few rows are bound by W's bytes, and run at or above a large copy's rate (5.1 TB/s;
 // several of these sizes stay in the last-level cache): 16 x 28672 x 8192 42.1 us a call,
 // 5.6 TB/s; 64 x 8192 x 8192 12.9, 5.3.  1 x 4096 x 4096 takes 4.5 in the kernel, 6.7 a call.
-// Many rows are bound by what a compute unit gets from the caches: 8192 x 8192 x 8192 451 us,
-// 2438 TOP/s, where without its loads the kernel took 360 and without its products 430, and the
+// Many rows are bound by what a compute unit gets from the caches: 8192 x 8192 x 8192 458 us,
+// 2400 TOP/s, where without its loads the kernel took 360 and without its products 430, and the
 // matrix cores alone 233; the library's product of these integers (without scales) takes 496.
 // Measured there and not kept: half-width steps, four of them in LDS (500 us: half lines
 // load at half the rate); the two wavefronts of a SIMD in turns of reading and

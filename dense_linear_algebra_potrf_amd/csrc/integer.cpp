@@ -217,9 +217,9 @@ batchlas_status do_block_norm_grad(int type, bl::BlockGradArgs a, int64_t gates,
 extern "C" {
 
 batchlas_status batchlas_integer_quant(batchlas_type type, int64_t rows, int64_t n, const void* x,
-                                    int64_t ldx, const float* given, int8_t* q, int64_t ldq,
-                                    float* scales, void* values, int64_t ldv,
-                                    batchlas_stream_t stream) {
+                                       int64_t ldx, const float* given, int8_t* q, int64_t ldq,
+                                       float* scales, void* values, int64_t ldv,
+                                       batchlas_stream_t stream) {
     return guarded([&] {
         return do_int8_quant(type, {rows, n, x, ldx, given, q, ldq, scales, values, ldv},
                              reinterpret_cast<hipStream_t>(stream));
@@ -227,9 +227,9 @@ batchlas_status batchlas_integer_quant(batchlas_type type, int64_t rows, int64_t
 }
 
 batchlas_status batchlas_integer_matmul(batchlas_type ytype, int64_t m, int64_t n, int64_t k,
-                                     const int8_t* x, int64_t ldx, const float* xscales,
-                                     const int8_t* w, int64_t ldw, const float* wscales, void* y,
-                                     int64_t ldy, batchlas_stream_t stream) {
+                                        const int8_t* x, int64_t ldx, const float* xscales,
+                                        const int8_t* w, int64_t ldw, const float* wscales, void* y,
+                                        int64_t ldy, batchlas_stream_t stream) {
     return guarded([&] {
         return do_int8_matmul(ytype, {m, n, k, x, ldx, xscales, w, ldw, wscales, y, ldy},
                               reinterpret_cast<hipStream_t>(stream));

@@ -377,9 +377,9 @@ batchlas_status batchlas_weight_matvec_workspace(int64_t m, int64_t k, int64_t *
  * not written.
  */
 batchlas_status batchlas_integer_quant(batchlas_type type, int64_t rows, int64_t n, const void *x,
-                                    int64_t ldx, const float *given, int8_t *q, int64_t ldq,
-                                    float *scales, void *values, int64_t ldv,
-                                    batchlas_stream_t stream);
+                                       int64_t ldx, const float *given, int8_t *q, int64_t ldq,
+                                       float *scales, void *values, int64_t ldv,
+                                       batchlas_stream_t stream);
 
 /*
  * integer_matmul: y[i, j] = xscales[i] * wscales[j] * sum_c x[i, c] * w[j, c], x (m x k)
@@ -391,9 +391,9 @@ batchlas_status batchlas_integer_quant(batchlas_type type, int64_t rows, int64_t
  * beyond 2^36, ldx or ldw beyond 2^22.
  */
 batchlas_status batchlas_integer_matmul(batchlas_type ytype, int64_t m, int64_t n, int64_t k,
-                                     const int8_t *x, int64_t ldx, const float *xscales,
-                                     const int8_t *w, int64_t ldw, const float *wscales, void *y,
-                                     int64_t ldy, batchlas_stream_t stream);
+                                        const int8_t *x, int64_t ldx, const float *xscales,
+                                        const int8_t *w, int64_t ldw, const float *wscales, void *y,
+                                        int64_t ldy, batchlas_stream_t stream);
 
 /*
  * block_norm: from a block's output y and the residual x to the next block's

@@ -761,3 +761,43 @@ def test_more_rows_than_a_launch_has_groups(n):
     for part in parts:
         for a, b in zip((dy, dx), bl.block_norm_grad(v[part], y[part], h[part], w, p, g)):
             assert torch.equal(a[part], b)
+
+
+def test_calls_at_once_on_two_streams():
+    """Steps that run beside each other on two streams, each with what it allocates, give the bits of one alone."""
+    import torch
+    import dense_linear_algebra_potrf_amd as bl
+    announce("integer layer: two streams at once")
+    states = [layer_state(40 + i, m=700 + 13 * i, n=900, k=2000) for i in range(2)]
+    want = [raw(layer_step(bl, s)) for s in states]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        got = [layer_step(bl, s, stream=stream) for s, stream in zip(states, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert all(torch.equal(x, y) for x, y in zip(a, raw(b)))
+
+
+@pytest.mark.parametrize("shape", [(1000,), (3, 1000), (2, 5, 1000), (0, 1000), (2, 0, 1000)])
+def test_any_number_of_dimensions(shape):
+    """Rows of any shape, of a width that leaves padding, through the whole layer."""
+    import torch
+    import dense_linear_algebra_potrf_amd as bl
+    announce("integer layer: dimensions", shape)
+    rows, k = int(np.prod(shape[:-1])), shape[-1]
+    s = layer_state(60, m=max(rows, 1), n=48, k=k)
+    flat = {key: s[key][:rows] for key in ("y", "x", "dv", "dh")}
+    wq, ws, _ = bl.int8_quant(s["W"])
+    q, qs, h = bl.block_norm(flat["y"].view(shape), flat["x"].view(shape), s["w"], s["p"], s["g"], int8=True)
+    z = bl.int8_matmul(q, wq, qs, ws)
+    assert q.shape == h.shape == shape and qs.shape == (rows,) and z.shape == (*shape[:-1], 48)
+    q2, qs2, h2 = bl.block_norm(flat["y"], flat["x"], s["w"], s["p"], s["g"], int8=True)
+    assert torch.equal(q.reshape(rows, k), q2) and torch.equal(qs, qs2) and torch.equal(h.view(rows, k), h2)
+    assert torch.equal(z.view(rows, 48), bl.int8_matmul(q2, wq, qs2, ws))
+    got = bl.block_norm_grad(*(flat[key].view(shape) for key in ("dv", "y")), h, s["w"], s["p"], s["g"], flat["dh"].view(shape))
+    want = bl.block_norm_grad(flat["dv"], flat["y"], h2, s["w"], s["p"], s["g"], flat["dh"])
+    assert got[0].shape == got[1].shape == shape
+    assert all(torch.equal(a.reshape(b.shape), b) for a, b in zip(got, want))
+    c, cs, values = bl.int8_quant(flat["x"].view(shape), values=True)
+    assert c.shape == values.shape == shape and cs.shape == (rows,)
