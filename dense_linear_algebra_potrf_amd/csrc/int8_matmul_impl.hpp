@@ -410,7 +410,8 @@ inline hipError_t few(const Int8MatmulArgs& a, hipStream_t s) {
 // the rounds those in which its workgroups go over the 256 compute units and the steps
 // those of 128 columns.  The constants are fitted to each variant's times at 190 sizes
 // from 1 x 64 x 64 to 8192 x 28672 x 16384 (within 8 to 16% on average); what is
-// chosen takes 1.8% more than the best of them on average, at most 1.5 times.  In us:
+// chosen takes 1.8% more than the best of them on average, at most 1.5 times.  In us, to bf16
+// and through the caches (past them the larger ones take 1 to 8% less):
 //     1 x 4096 x 4096        1 x 1 tiles 4.5, 1 x 2 4.6, 1 x 4 5.6
 //     1 x 28672 x 8192       1 x 1 45.0, 1 x 2 50.2, 1 x 4 40.9
 //     32 x 8192 x 8192       2 x 2 11.8, 2 x 4 12.5, 4 x 2 12.0
