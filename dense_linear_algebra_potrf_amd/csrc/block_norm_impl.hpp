@@ -43,7 +43,7 @@ __device__ __forceinline__ float unit_factor(float (&v)[VPT][8], int n, float ep
         for (int i = 0; i < VPT; ++i)
 #pragma unroll
             for (int j = 0; j < 8; ++j) most = Max{}(most, magnitude(v[i][j]));
-        const float f = rescale(block_reduce<TPR>(most, Max{}, tops));
+        const float f = rescale(block_reduce<TPR>(most, Max{}, tops), eps);
         sum = 0;
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
@@ -446,8 +446,8 @@ __global__ __launch_bounds__(Shape<TPR>::threads) void block_grad_kernel(BlockGr
                 }
                 in_turn();
             }
-            f = rescale(block_reduce<TPR>(most, Max{}, tops[parity][0]));
-            if constexpr (POST) yf = rescale(block_reduce<TPR>(ymost, Max{}, tops[parity][1]));
+            f = rescale(block_reduce<TPR>(most, Max{}, tops[parity][0]), a.eps);
+            if constexpr (POST) yf = rescale(block_reduce<TPR>(ymost, Max{}, tops[parity][1]), a.eps);
             sum = reduce<TPR, POST>(sum_up(f, yf), again[parity]);
             mean = sum.h2 / float(n) + a.eps * f * f;
             if constexpr (POST) ymean = sum.y2 / float(n) + a.eps * yf * yf;

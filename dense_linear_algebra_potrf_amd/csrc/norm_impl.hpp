@@ -26,11 +26,14 @@ template <int TPR> struct Shape {
 // sum is taken again of h times a power of two that brings the largest to about
 // 1.  The branch is the same for all threads of a row.
 __device__ __forceinline__ bool mean_in_range(float mean) { return mean > 0x1p-90f && mean < 0x1p90f; }
-// That power of two (a large one for a row of zeros: eps alone may be too small for
-// the root); 1 for a row that is not finite.
-__device__ __forceinline__ float rescale(uint32_t top) {
+// That power of two, f, for a row whose largest magnitude has the bits `top`; 1 for a row that
+// is not finite.  It brings the larger of that and sqrt(eps) to 1..2, so that eps f^2 stays
+// below 4 whatever eps is, and the mean, then eps f^2 + mean((h f)^2), above 1 / n: squares
+// that underflow beside such an eps do not count.
+__device__ __forceinline__ float rescale(uint32_t top, float eps) {
     if (top >= kInfBits) return 1.0f;
-    const int e = 127 - int(top >> 23);            // -127..127, kept where f and eps f^2 are finite
+    const uint32_t most = Max{}(top, __builtin_bit_cast(uint32_t, __builtin_amdgcn_sqrtf(eps)));
+    const int e = 127 - int(most >> 23);           // -127..127, kept where f is normal; rows of zeros without eps: 100
     return __builtin_bit_cast(float, uint32_t((e < -126 ? -126 : e < 100 ? e : 100) + 127) << 23);
 }
 

@@ -63,7 +63,7 @@ __global__ __launch_bounds__(Shape<TPR>::threads) void rmsnorm_quant_kernel(Norm
             for (int i = 0; i < VPT; ++i)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) most = Max{}(most, magnitude(v[i][j]));
-            const float f = rescale(block_reduce<TPR>(most, Max{}, tops[0]));
+            const float f = rescale(block_reduce<TPR>(most, Max{}, tops[0]), a.eps);
             sum = 0;
 #pragma unroll
             for (int i = 0; i < VPT; ++i)
@@ -197,7 +197,7 @@ __global__ __launch_bounds__(Shape<TPR>::threads) void rmsnorm_grad_kernel(NormG
             for (int i = 0; i < VPT; ++i)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) most = Max{}(most, magnitude(hr[i][j]));
-            f = rescale(block_reduce<TPR>(most, Max{}, tops));
+            f = rescale(block_reduce<TPR>(most, Max{}, tops), a.eps);
             square = dot = 0;
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
