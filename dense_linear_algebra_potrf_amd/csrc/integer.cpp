@@ -88,11 +88,11 @@ batchlas_status do_int8_matmul(int ytype, const bl::Int8MatmulArgs& a, hipStream
                           "integer_matmul launch");
 }
 
-// Rows of a gate; `per` becomes the rows that share one.
+// Rows of a gate; `per` becomes the rows that share one.  An empty batch may have none.
 batchlas_status check_gate(int64_t rows, int64_t gates, int64_t& per) {
-    BL_REQUIRE(gates >= 1, "gates must be >= 1");
-    BL_REQUIRE(rows % gates == 0, "gates must divide rows");
-    per = rows / gates;
+    BL_REQUIRE(gates >= 1 || (gates == 0 && rows == 0), "gates must be >= 1");
+    BL_REQUIRE(gates == 0 || rows % gates == 0, "gates must divide rows");
+    per = gates ? rows / gates : 0;
     return BATCHLAS_OK;
 }
 

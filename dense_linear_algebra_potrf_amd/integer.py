@@ -129,7 +129,7 @@ def _gate(gate, rows: int, n: int, dtype):
     if gate is None:
         return None, 0, 0
     gates, gn, ldg = _rows(gate, "gate", dtype)
-    if gn != n or gates < 1 or rows % gates:
+    if gn != n or (rows % gates if gates else rows):
         raise ValueError(f"gate must have {n} columns and a number of rows that divides {rows}, not {gates} x {gn}")
     return gate.data_ptr(), gates, ldg
 

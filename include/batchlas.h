@@ -408,7 +408,7 @@ batchlas_status batchlas_integer_matmul(batchlas_type ytype, int64_t m, int64_t 
  *            a scale a row, as integer_quant rounds it (ldv a multiple of 16)
  *   gate     gates x n; each row of it is that of rows / gates consecutive rows;
  *            NULL: none, and gates is not read
- *   gates    divides rows
+ *   gates    divides rows; 0 where rows is 0 and the gate has a row for each
  *   h        may be y or x itself (same leading dimension)
  *   eps      >= 0;  residual_scale finite
  * A row whose v is not finite gets a NaN scale and codes of zero.  n is at most
