@@ -52,6 +52,7 @@ def calibrate_weights(W, H, *, format: str = "int4", group: int | None = None, z
     return round_to(_compensated(W, H, group, lambda part: round_to(part)[3]))
 
 
+@torch.no_grad()
 def calibrate_channels(W, H, *, group: int = 64):
     """Round W [n, k] to 8-bit integers with a scale for each channel (row) against the second moments H of its inputs.
 

@@ -1,6 +1,10 @@
 """Binding of the 8-bit-integer layer operators (include/batchlas.h, "8-bit-integer
 layer operators"): argument checks and marshalling only, as in layer.py, whose
-conventions on tensors, streams and gradients hold here too.
+conventions on tensors and streams hold here too.
+
+Nothing is recorded for automatic differentiation.  int8_matmul, block_norm and
+int8_quant with values refuse floating tensors whose gradient or tangent would be
+lost; the norms' gradient is block_norm_grad, and codes have none.
 
 Rows of int8 codes are held in whole 16 bytes: a code tensor [rows, n] is, where n is
 not a multiple of 16, a view of the first n columns of a wider one, as int8_quant
@@ -64,6 +68,10 @@ def int8_quant(x, *, given=None, values=False, out=None, scales=None, stream=Non
         return _on(stream, int8_quant, x, given=given, values=values, out=out, scales=scales)
     lib = _layer._lib or _layer._bind()
     ty = _float_type(x, "x")
+    if values is False:
+        values = None
+    if values is not None:
+        _refuse_gradients(x, given)
     at = _gpu(x)
     rows, n, ldx = _rows(x, "x")
     if out is None:
@@ -81,11 +89,9 @@ def int8_quant(x, *, given=None, values=False, out=None, scales=None, stream=Non
             scales = x.new_empty(rows, dtype=_F32)
         sp = _vector(scales, "scales", _F32, rows)
     vp, ldv = None, 0
-    if values is True:
-        values = torch.empty_like(x)
-    elif values is False:
-        values = None
     if values is not None:
+        if values is True:
+            values = torch.empty_like(x)
         ldv = _rows(values, "values", x.dtype, (rows, n))[2]
         vp = values.data_ptr()
     s = _place(at, (out, given, scales, values))
