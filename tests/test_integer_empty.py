@@ -9,9 +9,9 @@ from tests.test_integer_abi import GRAD, NORM, P, call, lib  # noqa: F401
 
 @pytest.mark.parametrize("gate", [None, P])
 def test_no_rows_and_no_gates(lib, gate):  # noqa: F811
-    assert call(lib, "block_norm", NORM, dict(rows=0, gates=0, gate=gate)) == (0, "")
+    assert call(lib, "block_norm", NORM, dict(rows=0, gates=0, gate=gate))[0] == 0
     none = dict(rows=0, gates=0, gate=gate, dgate=None, dw=None, dpost=None, workspace=None, bytes=0)
-    assert call(lib, "block_norm_grad", GRAD, none) == (0, "")
+    assert call(lib, "block_norm_grad", GRAD, none)[0] == 0
 
 
 def test_rows_without_gates_are_refused(lib):  # noqa: F811
