@@ -134,9 +134,11 @@ batchlas_status do_rmsnorm_grad(int type, const bl::NormGradArgs& a, int64_t byt
                           "rmsnorm_grad launch");
 }
 
-batchlas_status do_weight_quant(int type, int format, int64_t group, const bl::WeightQuantArgs& a,
+batchlas_status do_weight_quant(int type, int format, int64_t group, bl::WeightQuantArgs a,
                                 hipStream_t stream) {
     BL_REQUIRE(is_float(type), "type must be F32, F16 or BF16");
+    const bool whole = format & BATCHLAS_FORMAT_WHOLE_ROWS;
+    format &= ~int(BATCHLAS_FORMAT_WHOLE_ROWS);
     batchlas_status st = check_format(format, group);
     if (st != BATCHLAS_OK) return st;
     BL_REQUIRE(a.n >= 1, "n must be >= 1");
@@ -159,6 +161,7 @@ batchlas_status do_weight_quant(int type, int format, int64_t group, const bl::W
                "an array is not aligned to its element size");
     st = bl::check_device();
     if (st != BATCHLAS_OK) return st;
+    if (whole) a.held = (a.k + 31) / 32 * 16;
     return bl::hip_status(bl::weight_quant(static_cast<Type>(type), static_cast<Format>(format),
                                            int(group), a, stream),
                           "weight_quant launch");
@@ -278,7 +281,7 @@ batchlas_status batchlas_weight_quant(batchlas_type type, batchlas_format format
                                       batchlas_stream_t stream) {
     return guarded([&] {
         return do_weight_quant(type, format, group,
-                               {n, k, W, ldw, codes, ldc, scales, lds, zeros, ldz, values, ldv},
+                               {n, k, W, ldw, codes, ldc, scales, lds, zeros, ldz, values, ldv, 0},
                                reinterpret_cast<hipStream_t>(stream));
     });
 }

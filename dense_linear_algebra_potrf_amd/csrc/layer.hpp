@@ -50,6 +50,7 @@ struct WeightQuantArgs {
     void* scales; int64_t lds;
     uint8_t* zeros; int64_t ldz;         // may be null
     void* values; int64_t ldv;           // may be null
+    int64_t held;                        // bytes of a row that are written; 0: those with codes
 };
 hipError_t weight_quant(Type t, Format f, int group, const WeightQuantArgs& a, hipStream_t s);
 

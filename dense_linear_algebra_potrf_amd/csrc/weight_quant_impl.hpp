@@ -105,10 +105,11 @@ __global__ __launch_bounds__(256) void weight_quant_kernel(WeightQuantArgs a, in
                 if constexpr (ZEROS) a.zeros[row * a.ldz + g] = uint8_t(z);
             }
         }
-        if (left <= 0) continue;
-        if (left < 8) codes &= (1u << (4 * left)) - 1;         // the half byte past an odd k
+        const bool whole = c / 2 < a.held;                      // what has no codes is written too
+        if (left <= 0 && !whole) continue;
+        if (left < 8) codes &= left > 0 ? (1u << (4 * left)) - 1 : 0;   // the half byte past an odd k, and the padding
         uint8_t* out = a.codes + row * a.ldc + c / 2;
-        if (left >= 7) {
+        if (left >= 7 || whole) {
             *reinterpret_cast<uint32_t*>(out) = codes;
         } else {
 #pragma unroll

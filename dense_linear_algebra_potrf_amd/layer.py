@@ -19,6 +19,7 @@ from torch.autograd import forward_ad
 
 _TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2, torch.float8_e4m3fn: 3}
 _FORMATS = {"int4": 0, "fp4": 1}
+_WHOLE_ROWS = 16                # added to a format
 _SCALES = {"row": 1, "block": 2}
 _E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
 
@@ -246,6 +247,7 @@ def weight_quant(W, *, format: str = "int4", group: int | None = None, zeros: bo
                    codes=codes, scales=scales, zeros_out=zeros_out)
     lib = _lib or _bind()
     ty = _float_type(W, "W")
+    whole = 0
     at = _gpu(W)
     n, k, ldw = _rows(W, "W")
     st_type = _scale_type(format)
@@ -256,8 +258,7 @@ def weight_quant(W, *, format: str = "int4", group: int | None = None, zeros: bo
     groups = -(-k // group)
     if codes is None:
         codes = W.new_empty((n, (k + 31) // 32 * 16), dtype=torch.uint8)
-        if k % 32:                                              # the same bytes on every run, the padding too
-            codes[:, (k + 1) // 2:].zero_()
+        whole = _WHOLE_ROWS                                     # the same bytes on every run, the padding too
     if codes.shape[0] != n:
         raise ValueError(f"codes must have {n} rows")
     ldc = _codes(codes, k)[1]
@@ -281,7 +282,7 @@ def weight_quant(W, *, format: str = "int4", group: int | None = None, zeros: bo
         ldv = _rows(values, "values", W.dtype, (n, k))[2]
         vp = values.data_ptr()
     s = _place(at, (codes, scales, zeros_out, values))
-    st = lib.batchlas_weight_quant(ty, _FORMATS[format], group, n, k, W.data_ptr(), ldw, codes.data_ptr(), ldc,
+    st = lib.batchlas_weight_quant(ty, _FORMATS[format] + whole, group, n, k, W.data_ptr(), ldw, codes.data_ptr(), ldc,
                                    scales.data_ptr(), lds, zp, ldz, vp, ldv, s)
     if st:
         _check(st)

@@ -245,7 +245,8 @@ typedef enum {
 
 typedef enum {
     BATCHLAS_FORMAT_INTEGER = 0,
-    BATCHLAS_FORMAT_FLOAT = 1
+    BATCHLAS_FORMAT_FLOAT = 1,
+    BATCHLAS_FORMAT_WHOLE_ROWS = 16   /* added to either in weight_quant */
 } batchlas_format;
 
 /*
@@ -309,7 +310,8 @@ batchlas_status batchlas_rmsnorm_grad_workspace(batchlas_type type, int64_t rows
  *            stored
  * A group that holds a weight that is not finite, or whose hi - lo overflows,
  * gets a NaN scale, codes of zero (and z = 8) and NaN values.  The unused half byte of an odd k is a code
- * of zero; bytes beyond (k + 1) / 2 of a row are not written.
+ * of zero.  Bytes beyond (k + 1) / 2 of a row are not written; with WHOLE_ROWS
+ * added to the format, those of the row's last 16 are set to zero.
  */
 batchlas_status batchlas_weight_quant(batchlas_type type, batchlas_format format, int64_t group,
                                       int64_t n, int64_t k, const void *W, int64_t ldw,
