@@ -262,7 +262,8 @@ typedef enum {
  *   eps      >= 0
  *   lds      >= (n + 31) / 32 for BLOCK; not read for ROW
  * A row (block) that holds a v that is not finite gets a NaN scale and NaN
- * values; a row of zeros gets the smallest scale and zeros.
+ * values; a row of zeros gets the smallest scale and zeros, or with eps = 0, where
+ * it is 0 / 0, a NaN scale and NaN values.
  * n is at most 32768, else NOT_SUPPORTED.
  */
 batchlas_status batchlas_rmsnorm_quant(batchlas_type type, batchlas_scale scale, int64_t rows,
@@ -413,7 +414,9 @@ batchlas_status batchlas_integer_matmul(batchlas_type ytype, int64_t m, int64_t 
  *   gates    divides rows; 0 where rows is 0 and the gate has a row for each
  *   h        may be y or x itself (same leading dimension)
  *   eps      >= 0;  residual_scale finite
- * A row whose v is not finite gets a NaN scale and codes of zero.  n is at most
+ * A row whose v is not finite gets a NaN scale and codes of zero.  A row of zeros
+ * stays zero (the smallest scale and codes of zero) where eps is not 0; where it
+ * is, the row has no root and is NaN, here and in the gradient.  n is at most
  * 32768, else NOT_SUPPORTED.
  */
 batchlas_status batchlas_block_norm(batchlas_type type, batchlas_scale scale, int64_t rows,

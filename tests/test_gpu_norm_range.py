@@ -99,3 +99,28 @@ def test_eps_beyond_the_range_of_squares(t, n):
     want = ref.block_norm_grad(*f64s(dv, y, x, w), None, None, None, 1.0, eps)
     close(dx, *want["dx"], "dx")
     close(dw, *want["dweight"], "dweight")
+
+
+@pytest.mark.parametrize("t", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("n", [60, 700, 5000, 16000])
+def test_a_row_of_zeros_without_eps_has_no_root(t, n):
+    """eps = 0: a row of zeros is 0 / 0, as in the definition, and stays in its row (and in the sums over rows)."""
+    import torch
+    import dense_linear_algebra_potrf_amd as bl
+    announce("norms, rows of zeros without eps", t, n)
+    y, x, w, p, g = norm_inputs(25, dtype(t), 4, n, True, 0)
+    x[1] = y[1] = 0                                # both norms of it
+    y[2] = 0                                       # the first alone, where there is one
+    for post in (p, None):
+        lost = [1, 2] if post is not None else [1]
+        kept = [i for i in range(4) if i not in lost]
+        v, _, h = bl.block_norm(y, x, w, post, eps=0.0)
+        q, s, h8 = bl.block_norm(y, x, w, post, eps=0.0, int8=True)
+        assert torch.equal(torch.nan_to_num(h), torch.nan_to_num(h8))
+        assert bool(v[lost].isnan().all()) and bool(s[lost].isnan().all()) and not q[lost].any()
+        assert bool(h[1].isnan().all()) if post is not None else not h[1].any()
+        assert bool(v[kept].isfinite().all()) and bool(s[kept].isfinite().all()) and bool(h[kept].isfinite().all())
+        dy, dx, _, dw, dp = bl.block_norm_grad(x, y, x, w, post, eps=0.0)
+        assert bool(dx[1].isnan().all()) and bool(dw.isnan().all()) and bool(dx[[0, 2, 3]].isfinite().all())
+        assert bool(dy[lost].isnan().all()) and bool(dy[kept].isfinite().all())
+        assert dp is None or bool(dp.isnan().all())
