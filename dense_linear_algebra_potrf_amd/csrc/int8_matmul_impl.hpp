@@ -280,6 +280,7 @@ __global__ __launch_bounds__(64 * WM * WN) void int8_tiles_kernel(Int8MatmulArgs
 // for nobody until they join their sums.
 template <typename T, int MB, int NB, int WAVES, int DEPTH>
 __global__ __launch_bounds__(64 * WAVES) void int8_few_kernel(Int8MatmulArgs a) {
+    static_assert(DEPTH >= 2 && DEPTH <= 4, "the waits at a wavefront's last steps");
     constexpr int TILES = MB + NB, LOADS = 2 * TILES;
     constexpr int JOIN = WAVES * MB * NB * 64 * 16, RING = WAVES * DEPTH * TILES * kTile;
     __shared__ __attribute__((aligned(16))) int8_t lds[JOIN > RING ? JOIN : RING];
@@ -356,8 +357,6 @@ __global__ __launch_bounds__(64 * WAVES) void int8_few_kernel(Int8MatmulArgs a) 
     for (int i = 0; i < mine; ++i) {
         const int after = mine - 1 - i;
         if (after >= DEPTH - 2) wait_loads<LOADS * (DEPTH - 2)>();      // its i-th is there, what was before has been read
-        else if (DEPTH > 5 && after == 3) wait_loads<LOADS * 3>();
-        else if (DEPTH > 4 && after == 2) wait_loads<LOADS * 2>();
         else if (DEPTH > 3 && after == 1) wait_loads<LOADS>();
         else wait_loads<0>();
         if (after >= DEPTH - 1) load(i + DEPTH - 1, at == 0 ? DEPTH - 1 : at - 1);
