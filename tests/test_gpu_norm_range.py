@@ -124,3 +124,26 @@ def test_a_row_of_zeros_without_eps_has_no_root(t, n):
         assert bool(dx[1].isnan().all()) and bool(dw.isnan().all()) and bool(dx[[0, 2, 3]].isfinite().all())
         assert bool(dy[lost].isnan().all()) and bool(dy[kept].isfinite().all())
         assert dp is None or bool(dp.isnan().all())
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("n", WIDTHS)
+def test_gradient_where_means_cancel(t, n):
+    """Without a residual h is g p y t itself, so that the gradient that comes through its norm has no part along
+    y, and the sums from which that mean is put together cancel; and dv along h, of which the norm leaves nothing."""
+    import torch
+    import dense_linear_algebra_potrf_amd as bl
+    announce("block_norm_grad, means that cancel", t, n)
+    dv, y, x, w, p, g, _ = grad_inputs(26, dtype(t), 6, n, True, 2, False)
+    y[3:] = y[3:].abs() + 1                            # sums that do not average out either
+    h = bl.block_norm(y, x, w, p, g, residual_scale=0.0)[2]
+    along = (h.float() / w.float()).to(dtype(t))
+    for grad in (dv, along, along * 100):
+        for part in (None, 1e-3 * grad):
+            inputs = (grad, y, h, w, p, g, part)
+            with np.errstate(all="ignore"):
+                want = ref.block_norm_grad(*f64s(*inputs), 0.0, 1e-6)
+            got = bl.block_norm_grad(*inputs, residual_scale=0.0)
+            for name, out in zip(NAMES, got):
+                close(out, *want[name], name)
+            assert not got[1].any()
