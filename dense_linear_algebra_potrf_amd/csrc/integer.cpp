@@ -138,6 +138,7 @@ batchlas_status do_block_norm(int type, int scale, bl::BlockNormArgs a, int64_t 
                "an array is not aligned to its element size");
     st = check_norm_width(a.n, bl::kBlockNormMaxN);
     if (st != BATCHLAS_OK || a.rows == 0) return st;
+    BL_REQUIRE(a.h != a.v, "h and v must be different");
     st = bl::check_device();
     if (st != BATCHLAS_OK) return st;
     return bl::hip_status(bl::block_norm(static_cast<Type>(type), static_cast<Scale>(scale), a,
@@ -205,6 +206,7 @@ batchlas_status do_block_norm_grad(int type, bl::BlockGradArgs a, int64_t gates,
         BL_POINTER(a.workspace, "workspace");
         BL_REQUIRE(bytes >= need, "workspace_bytes is less than block_norm_grad_workspace gives");
     }
+    BL_REQUIRE(a.rows == 0 || a.dy != a.dx, "dy and dx must be different");
     if (a.rows == 0 && !a.dw && !a.dpost && !a.dgate) return BATCHLAS_OK;
     st = bl::check_device();
     if (st != BATCHLAS_OK) return st;

@@ -206,7 +206,7 @@ def block_norm_grad(dv, y, h, weight, post_weight=None, gate=None, dh=None, *, r
 
     dv is the gradient of v (before a rounding to 8 bits), dh the one that reaches h
     on the residual path.  dy and dx (of the residual) have y's type and may each be
-    dv, y, h or dh itself.  dgate has gate's shape and type, or float32 for a gate
+    dv, y, h or dh itself, not one another.  dgate has gate's shape and type, or float32 for a gate
     [n]; dweight and dpost_weight are float32 [n].  Each of the three is not computed
     where False is passed, and None where there is no such input.  workspace: a uint8
     tensor of block_norm_grad_workspace(...) bytes, allocated by the call where it is

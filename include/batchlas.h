@@ -412,7 +412,7 @@ batchlas_status batchlas_integer_matmul(batchlas_type ytype, int64_t m, int64_t 
  *   gate     gates x n; each row of it is that of rows / gates consecutive rows;
  *            NULL: none, and gates is not read
  *   gates    divides rows; 0 where rows is 0 and the gate has a row for each
- *   h        may be y or x itself (same leading dimension)
+ *   h        may be y or x itself (same leading dimension), not v
  *   eps      >= 0;  residual_scale finite
  * A row whose v is not finite gets a NaN scale and codes of zero.  A row of zeros
  * stays zero (the smallest scale and codes of zero) where eps is not 0; where it
@@ -440,7 +440,8 @@ batchlas_status batchlas_block_norm(batchlas_type type, batchlas_scale scale, in
  *   dh       NULL: zero
  *   dgtype   of dgate: F32 or the type
  *   dw, dpost, dgate   NULL: not computed; dpost needs post, dgate a gate
- *   dy, dx   may each be dv, y, h or dh itself (same leading dimension)
+ *   dy, dx   may each be dv, y, h or dh itself (same leading dimension), not one
+ *            another
  *   workspace  device memory of at least the bytes that
  *            batchlas_block_norm_grad_workspace gives, aligned to 4 bytes; not
  *            used (may be NULL) where that is 0
