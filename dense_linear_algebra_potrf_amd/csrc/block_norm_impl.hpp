@@ -645,7 +645,9 @@ inline hipError_t block_norm_t(Scale sc, const BlockNormArgs& a, hipStream_t s) 
     });
 }
 
-// Runs of rows: two workgroups a compute unit, or the one that it has registers for.  A
+// Runs of rows: 512 workgroups for rows of up to 256 threads (the shapes of one vector a thread have
+// registers for three a compute unit or more; what that would do for 513 to 768 rows, which are two
+// to a run now, was not measured), 256 for wider ones, which have room for one.  A
 // gate with more rows than a workgroup's groups of threads is cut into equal runs, whole
 // workgroups of them, so that its S is joined there; smaller ones are put together.  Runs
 // of one row, where there are few rows, cost the sums less than they save here: 64 rows

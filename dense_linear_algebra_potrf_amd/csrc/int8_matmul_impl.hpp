@@ -20,9 +20,11 @@
 // Few rows are bound by W's bytes, and run at or above a large copy's rate (5.1 TB/s;
 // several of these sizes stay in the last-level cache): 16 x 28672 x 8192 42.1 us a call,
 // 5.6 TB/s; 64 x 8192 x 8192 12.9, 5.3.  1 x 4096 x 4096 takes 4.5 in the kernel, 6.7 a call.
-// Many rows are bound by what a compute unit gets from the caches: 8192 x 8192 x 8192 458 us,
-// 2400 TOP/s, where without its loads the kernel took 360 and without its products 430, and the
-// matrix cores alone 233; the library's product of these integers (without scales) takes 496.
+// Many rows are bound by what a compute unit gets from the caches: 8192 x 8192 x 8192 454 us,
+// 2420 TOP/s, where without its loads the kernel took 360 and without its products 430, and the
+// matrix cores alone 233.  The clock goes by the codes and by what ran before: beside each other
+// on the same normal codes this takes 422 and the library's product of these integers (without
+// scales) 451; on codes uniform within -127..127 463, and launches apart, in a profile, 502 on average.
 // Measured there and not kept: half-width steps, four of them in LDS (500 us: half lines
 // load at half the rate); the two wavefronts of a SIMD in turns of reading and
 // multiplying (485); loads as whole-address loads, which the compiler lets every LDS
@@ -408,9 +410,10 @@ inline hipError_t few(const Int8MatmulArgs& a, hipStream_t s) {
 // The variant with the least estimated time: `fixed` + rounds (`round` + steps `step`) us,
 // the rounds those in which its workgroups go over the 256 compute units and the steps
 // those of 128 columns.  The constants are fitted to each variant's times at 190 sizes
-// from 1 x 64 x 64 to 8192 x 28672 x 16384 (within 8 to 16% on average); what is
-// chosen takes 1.8% more than the best of them on average, at most 1.5 times.  In us, to bf16
-// and through the caches (past them the larger ones take 1 to 8% less):
+// from 1 x 64 x 64 to 8192 x 28672 x 16384 (within 8 to 16% on average); what was
+// chosen took 1.8% more than the best of them on average, at most 1.5 times.  That was to bf16
+// and through the caches (past them the larger ones take 1 to 8% less), before 32-bit outputs were
+// dealt to lanes as they are; y's type is not in the estimate.  In us, as measured then:
 //     1 x 4096 x 4096        1 x 1 tiles 4.5, 1 x 2 4.6, 1 x 4 5.6
 //     1 x 28672 x 8192       1 x 1 45.0, 1 x 2 50.2, 1 x 4 40.9
 //     32 x 8192 x 8192       2 x 2 11.8, 2 x 4 12.5, 4 x 2 12.0

@@ -8,7 +8,7 @@ lost; the norms' gradient is block_norm_grad, and codes have none.
 
 Rows of int8 codes are held in whole 16 bytes: a code tensor [rows, n] is, where n is
 not a multiple of 16, a view of the first n columns of a wider one, as int8_quant
-and block_norm return it.
+and block_norm return it.  What is behind them may hold anything.
 """
 from __future__ import annotations
 
