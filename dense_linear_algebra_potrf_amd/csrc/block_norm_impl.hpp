@@ -457,7 +457,8 @@ __global__ __launch_bounds__(Shape<TPR>::threads) void block_grad_kernel(BlockGr
         [[maybe_unused]] float rt = 1, ts = 1, yback = 0;
         if constexpr (POST) {
             rt = inverse_root(ymean), ts = yf * rt;
-            yback = rt * ((sum.kd + s * (sum.ke - rs * (back * sum.kh))) / float(n));
+            // kh with rs first: with back, which has the gradients' size, it would leave the range before ke does
+            yback = rt * ((sum.kd + s * (sum.ke - back * (rs * sum.kh))) / float(n));
         }
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {

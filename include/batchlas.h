@@ -445,6 +445,8 @@ batchlas_status batchlas_block_norm(batchlas_type type, batchlas_scale scale, in
  *   workspace  device memory of at least the bytes that
  *            batchlas_block_norm_grad_workspace gives, aligned to 4 bytes; not
  *            used (may be NULL) where that is 0
+ * Sums over a row are held in 32 bits, of rows that are scaled where they are large
+ * or small; gradients (times w, post and gate) beyond about 1e26 may leave them.
  * n is at most 16384, else NOT_SUPPORTED.  rows may be 0: dw, dpost and dgate are
  * set to zero.
  */
